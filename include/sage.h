@@ -224,11 +224,118 @@ sage_status sage_selftest_wait_timeout(int budget_us, void* stream);
  * 1..1000000 or a NULL ops. */
 sage_status sage_mma_probe(int kind, int iters, double* ops, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Serving: what stands before and behind the attention of a language model.  The pages stop at the
+ * attention call (no counterpart there); the quantization is the one above, with the scales a cache
+ * can have that grows token by token: one per token and kv head.
+ *
+ * A decode step is sage_cache_append (norm, rotation, cache write) and sage_attn_decode; a prompt is
+ * sage_cache_append and, on its own 16-bit K and V, sage_attn_varlen; a prompt behind a cached prefix
+ * reads that prefix back with sage_cache_gather first.
+ * ---------------------------------------------------------------------------------------------- */
+
+/* RMS norm and position rotation of the heads, all in fp32 with one rounding at the end:
+ *   n_c = x_c * rsqrt(sum_c x_c^2 / d + eps) * w_c        (norm = 0: n = x; weights NULL: w = 1)
+ *   y_a = n_a cos_i - n_b sin_i,  y_b = n_b cos_i + n_a sin_i
+ * for i < rot / 2 and the channel pairs (a, b) = (i, i + rot / 2), or (2i, 2i + 1) when interleaved;
+ * channels at and behind rot pass.  Row p of cos_sin (n_pos rows of rot fp32) holds the rot / 2 cosines
+ * of position p, then the sines; NULL: no rotation.  q_weight and k_weight hold d values of
+ * weight_dtype (fp16, bf16 or fp32).  eps >= 0; rot even, 2 <= rot <= d.  cos_sin and fp32 weights are
+ * 4-byte aligned. */
+typedef struct {
+  int norm;
+  float eps;
+  const void* q_weight;
+  const void* k_weight;
+  sage_dtype weight_dtype;
+  const float* cos_sin;
+  int n_pos;
+  int rot;
+  int interleaved;
+} sage_norm_rope;
+
+/* Norm and rotation of every head of q (B, N, Hq, d) and k (B, N, Hkv, d) in one launch.  k may be NULL
+ * (Hkv is then ignored).  strides: 12 element strides >= 0, of the batches, tokens and heads of q, k,
+ * q_out and k_out, in that order (channels are contiguous), so that any layout goes, views of a fused
+ * projection among them.  positions: DEVICE int32 [B][N], rows pos_batch_stride elements apart (0: one row
+ * for all batches); NULL: token n is at position n.  A token whose position is not in 0 .. n_pos - 1 is
+ * left unwritten, and sage_check_status returns SAGE_ERR_INVALID_ARG.  q_out may be q and k_out may be k
+ * (same pointer and strides); outputs must not share other elements with an input or each other.
+ * N = 0 or B = 0 does nothing.  Allocates nothing. */
+sage_status sage_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+                              const int32_t* positions, long long pos_batch_stride, int B, int N, int Hq, int Hkv,
+                              int d, sage_dtype dtype, const sage_norm_rope* nr, void* stream);
+
+/* A paged cache of quantized K and V, device memory of the caller.  dc = 16 * ceil(d / 16); channels
+ * d .. dc-1 hold code 0.  page_size is a power of two, 16 .. 1024.  k8, v8 16-byte aligned.
+ *   k8  int8   [num_pages][Hkv][page_size][dc]      ks  fp32 [num_pages][Hkv][page_size]
+ *   v8  E4M3   [num_pages][Hkv][page_size][dc]      vs  fp32 [num_pages][Hkv][page_size]
+ * A page table is DEVICE int32 [B][max_pages], rows table_stride elements apart: position p of sequence b is in
+ * slot p % page_size of page page_table[b][p / page_size].  Entries behind a sequence's last page are not
+ * read.  An entry outside 0 .. num_pages-1 that is needed is reported by sage_check_status as
+ * SAGE_ERR_INVALID_ARG, and never followed. */
+typedef struct {
+  int8_t* k8;
+  float* ks;
+  uint8_t* v8;
+  float* vs;
+  int num_pages;
+  int page_size;
+  int Hkv;
+  int d;
+} sage_kv_cache;
+
+/* Quantizes new tokens into the cache.  k and v: (T, Hkv, d) packed tokens; cu_seqlens: DEVICE int32 [B + 1]
+ * non-decreasing offsets from 0 to at most T (sequence b owns tokens cu_seqlens[b] .. cu_seqlens[b+1]-1; tokens at and
+ * behind cu_seqlens[B] are left alone; a table that breaks this is reported by sage_check_status as
+ * SAGE_ERR_INVALID_ARG and the tokens that meet the fault are skipped), NULL: T = B, one token per sequence.  seq_lens: DEVICE int32 [B], the lengths WITH
+ * the new tokens: token i of sequence b goes to position seq_lens[b] - (new tokens of b) + i.  Without cu_seqlens,
+ * a sequence of length 0 is an empty slot of the batch and is skipped.  Per token and kv head, in fp32:
+ *   y = k - k_mean (k_mean: DEVICE fp32 [Hkv][d], NULL: 0; the same for all tokens of a head, it adds one
+ *   constant to all scores of a query, so attention is unchanged),  ks = amax / 127,
+ *   code = clamp(rint_even(y * (127 / amax)), -127, 127);
+ *   vs = amax / 448, code = E4M3_rne(v * (448 / amax)).
+ * A row with amax < 2^-100 gets scale 0 and codes 0, one that holds a NaN or an infinity scale NaN and codes 0.
+ * With nr, the keys are normed and rotated as by sage_qk_norm_rope at their position in the sequence first
+ * (fp32 up to the code), and so is q (T, Hq, d) into q_out; without q (NULL) Hq is ignored.  nr NULL: k is
+ * coded as it is, and q must be NULL.  strides: 8 element strides >= 0, of the tokens and heads of q, k, v and
+ * q_out.  q_out may be q.  A token whose position is negative, beyond the page table or (with nr) not in
+ * cos_sin is skipped and reported like a bad page.  Two tokens must not have the same place: where two
+ * sequences of one call share the page that both write, that place holds codes of either.
+ * T = 0 does nothing.  Allocates nothing. */
+sage_status sage_cache_append(const sage_kv_cache* cache, const void* q, const void* k, const void* v, void* q_out,
+                              const long long* strides, const int32_t* page_table, long long table_stride,
+                              int max_pages, const int32_t* seq_lens, const int32_t* cu_seqlens, const float* k_mean,
+                              int T, int B, int Hq, sage_dtype dtype, const sage_norm_rope* nr, void* stream);
+
+/* Reads cached tokens back: k_out and v_out (T, Hkv, d) contiguous, K = code * ks + k_mean and V = code * vs in
+ * fp32, rounded to dtype.  Token i of sequence b (cu_seqlens as above, not NULL) is position starts[b] + i
+ * (starts: DEVICE int32 [B], NULL: 0).  Rows at and behind cu_seqlens[B], and rows of bad places, are left
+ * unwritten.  The outputs must not overlap the cache or each other.  T = 0 does nothing.  Allocates nothing. */
+sage_status sage_cache_gather(const sage_kv_cache* cache, const int32_t* page_table, long long table_stride,
+                              int max_pages, const int32_t* cu_seqlens, const int32_t* starts, const float* k_mean,
+                              void* k_out, void* v_out, int T, int B, sage_dtype dtype, void* stream);
+
+/* Attention of one query token per sequence over its cached tokens:
+ *   out = softmax(q . K * sm_scale) V,  K = code * ks, V = code * vs
+ * q: (B, Hq, d) with element strides q_batch_stride and q_head_stride, out: (B, Hq, d) contiguous, of q's dtype.
+ * q is not quantized: scores, softmax and sums are fp32 on exact products of q and the codes.  seq_lens: DEVICE
+ * int32 [B], the keys each query sees (the new token's own key among them if it was appended); 0 gives zeros.
+ * max_seqlen >= 0 bounds them; a sequence longer than it or than its page table, or of negative length, is
+ * reported by sage_check_status as SAGE_ERR_INVALID_ARG and gets zeros; keys on a bad page are left out and
+ * reported.  Sequences may share pages.  Long sequences are split over the GPU and joined through a workspace
+ * from the pool that sage_attn uses (none for short ones); capture and errors as there.  The result does not
+ * depend on the run: nothing is summed in the order of arrival.  B = 0 does nothing. */
+sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long q_head_stride,
+                             const sage_kv_cache* cache, const int32_t* page_table, long long table_stride,
+                             int max_pages, const int32_t* seq_lens, void* out, int B, int Hq, int max_seqlen,
+                             sage_dtype dtype, float sm_scale, void* stream);
+
 /* Synchronizes `stream`, then reports (and clears) the device-side error word:
  * SAGE_ERR_TIMEOUT if a kernel gave up on a bounded wait, SAGE_ERR_BOUNDS if a
  * kernel of the checked build skipped a store outside its buffer (see
- * sage_checked_build), SAGE_ERR_INVALID_ARG for a flagged tile record or
- * cu_seqlens table, SAGE_ERR_CUDA for a pending CUDA error.  The error word is one per device, not per stream: it collects the
+ * sage_checked_build), SAGE_ERR_INVALID_ARG for a flagged tile record,
+ * cu_seqlens table, page, position or length, SAGE_ERR_CUDA for a pending CUDA error.  The error word is one per device, not per stream: it collects the
  * flags of every call on the current device since it was last read, whatever
  * stream they ran on, and the first sage_check_status to read it (on any stream)
  * reports and clears them.  Only `stream` is synchronized, so a call still
@@ -252,9 +359,9 @@ void sage_test_inject(int fake_cc, int fail_allocs);
 
 /* 1 for the checked build of this library (compiled with -DSAGE_CHECKED, shipped
  * beside the normal one as libsage_b200_checked.so), else 0.  In the checked build
- * every global-memory store of the quantize kernels and of the fused attention
- * kernel first tests that its bytes lie inside the buffer they belong to (sized as
- * this header states: out, the sage_quantize outputs, the workspace's parts); a
+ * every global-memory store of the quantize kernels, of the fused attention
+ * kernel and of the serving kernels first tests that its bytes lie inside the buffer they belong to (sized as
+ * this header states: out, the sage_quantize outputs, the cache, the workspace's parts); a
  * store outside is skipped, never made, and sage_check_status reports
  * SAGE_ERR_BOUNDS.  (The per-sequence table of packed batches and the tiles of
  * sage_qk_int32 are written at indices that their launch bounds: not checked.)

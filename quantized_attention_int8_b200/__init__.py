@@ -29,6 +29,7 @@ __all__ = [
     "SageError", "sage_attn", "sage_quantize", "sage_attn_quantized", "sage_qk_int32", "sage_check_status",
     "sage_workspace_bytes", "sage_device_supported", "sage_status_string", "padded_dim", "LIB_PATH", "capi",
     "sage_attn_noalloc", "SAGE_NOALLOC_MAX_BYTES", "load_checked", "CHECKED_LIB_PATH", "pv_mode", "sage_attn_varlen", "SageOpts", "opts",
+    "sage_qk_norm_rope", "sage_kv_cache", "sage_cache_append", "sage_cache_gather", "sage_attn_decode",
     "sageattn", "sageattn_qk_int8_pv_fp8_cuda", "sageattn_qk_int8_pv_fp16_cuda", "sageattn_varlen",
 ]
 
@@ -81,13 +82,26 @@ def opts(qk_quant_gran: str = "per_block", smooth_v: bool = False) -> SageOpts:
     return SageOpts(_GRANS[qk_quant_gran], 1 if smooth_v else 0)
 
 
+class SageNormRope(ctypes.Structure):
+    """The C ``sage_norm_rope``: RMS norm of the heads and their position rotation."""
+    _fields_ = [("norm", ctypes.c_int), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int), ("cos_sin", ctypes.c_void_p),
+                ("n_pos", ctypes.c_int), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class SageKVCache(ctypes.Structure):
+    """The C ``sage_kv_cache``: the four arrays of a paged cache and their sizes."""
+    _fields_ = [("k8", ctypes.c_void_p), ("ks", ctypes.c_void_p), ("v8", ctypes.c_void_p), ("vs", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int)]
+
+
 def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(
             f"{path} is not built; run `python quantized_attention_int8_b200/build_lib.py` "
             "(this package has no CPU fallback)")
     lib = ctypes.CDLL(path)
-    P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    P, I, F, Z, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
     sig = {
         "sage_attn": ([P, P, P, P, I, I, I, I, I, I, I, I, F, I, P], I),
         "sage_workspace_bytes": ([I, I, I, I, I], Z),
@@ -104,6 +118,10 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sage_test_inject": ([I, I], None),
         "sage_test_out_limit": ([ctypes.c_longlong], None),
         "sage_checked_build": ([], I),
+        "sage_qk_norm_rope": ([P, P, P, P, P, P, L, I, I, I, I, I, I, P, P], I),
+        "sage_cache_append": ([P, P, P, P, P, P, P, L, I, P, P, P, I, I, I, I, P, P], I),
+        "sage_cache_gather": ([P, P, L, I, P, P, P, P, P, I, I, I, P], I),
+        "sage_attn_decode": ([P, L, L, P, P, L, I, P, P, I, I, I, I, F, P], I),
         "sage_attn_varlen": ([P, P, P, P, P, P, I, I, I, ctypes.c_longlong, ctypes.c_longlong, I, I, I, I, I, F, I, P,
                               P], I),
     }
@@ -269,6 +287,260 @@ def sage_attn_noalloc(q, k, v, tensor_layout="HND", is_causal=False, sm_scale=No
                                 float(sm_scale) if sm_scale is not None else 0.0, pv_mode(pv_dtype, pv_accum_dtype),
                         _stream())
     _check(st, "sage_attn_noalloc")
+    return out
+
+
+# ---------------------------------------------------------------------------------------------
+# Serving: head norm and rotation, the paged cache, one-token attention (include/sage.h, "Serving").
+# None of these record gradients.
+# ---------------------------------------------------------------------------------------------
+def _call(device, name, *args):
+    """One C entry point on ``device`` and its current stream."""
+    if device.index == torch.cuda.current_device():
+        st = getattr(capi, name)(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(capi, name)(*args, torch.cuda.current_stream().cuda_stream)
+    _check(st, name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_heads(name, t, like=None):
+    """A CUDA tensor of 16-bit heads with contiguous channels, of the dtype and on the device of ``like``."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the channels (last dimension) of {name} must be contiguous")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have dtype {like.dtype} and be on {like.device}, got {t.dtype} on {t.device}")
+
+
+def _check_out(name, t, shape, like):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _check_heads(name, t, like)
+
+
+def _check_ints(name, t, shape, device):
+    """An int32 CUDA tensor of this shape (None: any extent) whose last dimension is contiguous."""
+    if not (t.is_cuda and t.dtype == torch.int32 and t.dim() == len(shape) and t.device == device):
+        raise ValueError(f"{name} must be a {len(shape)}-D int32 tensor on {device}")
+    if any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _norm_rope(d, device, norm, eps, q_weight, k_weight, cos_sin, interleaved) -> SageNormRope:
+    nr = SageNormRope(norm=int(bool(norm)), eps=float(eps), interleaved=int(bool(interleaved)))
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("q_weight and k_weight need norm=True")
+    dtypes = set()
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if not (w.is_cuda and w.device == device and w.dtype in _DTYPES and w.is_contiguous()
+                    and tuple(w.shape) == (d,)):
+                raise ValueError(f"{name} must be a contiguous fp16, bf16 or fp32 tensor of shape ({d},) on {device}")
+            dtypes.add(w.dtype)
+    if len(dtypes) > 1:
+        raise ValueError("q_weight and k_weight must share one dtype")
+    nr.q_weight, nr.k_weight = _ptr(q_weight), _ptr(k_weight)
+    nr.weight_dtype = _DTYPES[dtypes.pop()] if dtypes else SAGE_FP32
+    if cos_sin is not None:
+        if not (cos_sin.is_cuda and cos_sin.device == device and cos_sin.dtype == torch.float32
+                and cos_sin.dim() == 2 and cos_sin.is_contiguous()):
+            raise ValueError(f"cos_sin must be a contiguous 2-D float32 tensor (positions, rotary_dim) on {device}")
+        nr.cos_sin, nr.n_pos, nr.rot = cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
+    return nr
+
+
+def _btn(t, layout):
+    """(batches, tokens, heads) and their element strides of a 4-D HND / NHD or a 3-D packed tensor."""
+    if t.dim() == 3:
+        return (1, t.shape[0], t.shape[1]), (0, t.stride(0), t.stride(1))
+    if t.dim() != 4:
+        raise ValueError("q and k must be 4-D, or 3-D (tokens, heads, head_dim)")
+    if layout == "HND":
+        return (t.shape[0], t.shape[2], t.shape[1]), (t.stride(0), t.stride(2), t.stride(1))
+    if layout == "NHD":
+        return tuple(t.shape[:3]), tuple(t.stride()[:3])
+    raise ValueError(f"tensor_layout must be 'HND' or 'NHD', got {layout!r}")
+
+
+def sage_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weight=None, tensor_layout="HND", norm=True,
+                      eps=1e-6, interleaved=False, q_out=None, k_out=None):
+    """RMS norm of every query and key head and its position rotation in one launch; returns (q_out, k_out).
+
+    q (B,Hq,N,d), k (B,Hkv,N,d) (HND; NHD stores (B,N,H,d)), or packed tokens (T,H,d); channels contiguous,
+    otherwise any strides (slices of a fused projection).  k may be None.  cos_sin float32 (n_pos, rot): row p
+    holds the rot/2 cosines of position p's angles, then the sines; channels i and i + rot/2 turn together, or
+    2i and 2i + 1 with interleaved; None: no rotation.  positions int32 (N,) or (B,N), default 0..N-1; one
+    outside the table leaves its token unwritten and is reported by sage_check_status.  Weights (d,) in fp16,
+    bf16 or fp32.  q_out may be q and k_out may be k."""
+    _check_heads("q", q)
+    (B, N, Hq), qs = _btn(q, tensor_layout)
+    d = q.shape[-1]
+    Hkv, ks = 0, (0, 0, 0)
+    if k is not None:
+        _check_heads("k", k, q)
+        (Bk, Nk, Hkv), ks = _btn(k, tensor_layout)
+        if (Bk, Nk, k.shape[-1], k.dim()) != (B, N, d, q.dim()):
+            raise ValueError(f"k of shape {tuple(k.shape)} does not fit q of shape {tuple(q.shape)}")
+    pos_stride = 0
+    if positions is not None:
+        if cos_sin is None:
+            raise ValueError("positions need cos_sin")
+        _check_ints("positions", positions, (N,) if positions.dim() == 1 else (B, N), q.device)
+        pos_stride = positions.stride(0) if positions.dim() == 2 else 0
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _check_out("q_out", q_out, q.shape, q)
+    kos = (0, 0, 0)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        _check_out("k_out", k_out, k.shape, k)
+        kos = _btn(k_out, tensor_layout)[1]
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    nr = _norm_rope(d, q.device, norm, eps, q_weight, k_weight, cos_sin, interleaved)
+    strides = (ctypes.c_longlong * 12)(*qs, *ks, *_btn(q_out, tensor_layout)[1], *kos)
+    _call(q.device, "sage_qk_norm_rope", q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), strides,
+          _ptr(positions), pos_stride, B, N, Hq, Hkv, d, _DTYPES[q.dtype], ctypes.byref(nr))
+    return q_out, k_out
+
+
+def sage_kv_cache(num_pages, num_kv_heads, head_dim, page_size=64, device="cuda") -> dict:
+    """An empty paged cache: k8 int8 and v8 uint8 (E4M3 codes) (num_pages, Hkv, page_size, dc) with
+    dc = 16 * ceil(head_dim / 16), ks and vs float32 (num_pages, Hkv, page_size)."""
+    shape = (num_pages, num_kv_heads, page_size)
+    dc = (head_dim + 15) // 16 * 16
+    return dict(k8=torch.zeros((*shape, dc), dtype=torch.int8, device=device),
+                ks=torch.zeros(shape, dtype=torch.float32, device=device),
+                v8=torch.zeros((*shape, dc), dtype=torch.uint8, device=device),
+                vs=torch.zeros(shape, dtype=torch.float32, device=device))
+
+
+def _cache_struct(cache, d, device) -> SageKVCache:
+    k8, ks, v8, vs = cache["k8"], cache["ks"], cache["v8"], cache["vs"]
+    for name, t, dtype in (("k8", k8, torch.int8), ("v8", v8, torch.uint8), ("ks", ks, torch.float32),
+                           ("vs", vs, torch.float32)):
+        if not (t.is_cuda and t.device == device and t.dtype == dtype and t.is_contiguous()):
+            raise ValueError(f"cache[{name!r}] must be a contiguous {dtype} tensor on {device}")
+    if k8.dim() != 4 or k8.shape[3] != (d + 15) // 16 * 16:
+        raise ValueError(f"cache['k8'] of shape {tuple(k8.shape)} does not hold heads of {d} channels")
+    if v8.shape != k8.shape or ks.shape != k8.shape[:3] or vs.shape != k8.shape[:3]:
+        raise ValueError("the cache's arrays do not fit one another")
+    return SageKVCache(k8.data_ptr(), ks.data_ptr(), v8.data_ptr(), vs.data_ptr(), k8.shape[0], k8.shape[2],
+                       k8.shape[1], d)
+
+
+def _check_k_mean(k_mean, Hkv, d, device):
+    if k_mean is not None and not (k_mean.is_cuda and k_mean.device == device and k_mean.dtype == torch.float32
+                                   and tuple(k_mean.shape) == (Hkv, d) and k_mean.is_contiguous()):
+        raise ValueError(f"k_mean must be a contiguous float32 tensor of shape ({Hkv}, {d}) on {device}")
+
+
+def sage_cache_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, q=None, cos_sin=None, q_weight=None,
+                      k_weight=None, norm=False, eps=1e-6, interleaved=False, k_mean=None, q_out=None):
+    """Quantizes new tokens k, v (T,Hkv,d) into the paged cache (a dict as sage_kv_cache returns).
+
+    page_table int32 (B, max_pages), seq_lens int32 (B,): lengths with the new tokens; cu_seqlens int32 (B+1,): each
+    sequence's tokens in the packed k and v, None: one token per sequence (length 0: an empty slot, skipped).
+    norm, weights, cos_sin, interleaved: as sage_qk_norm_rope, on the keys at their positions, and on q (T,Hq,d),
+    which is returned (q_out; None without q).  k_mean float32 (Hkv,d) is subtracted from the keys before
+    they are coded.  Channels contiguous, other strides free.  Bad pages and positions are skipped and reported
+    by sage_check_status."""
+    _check_heads("k", k)
+    _check_heads("v", v, k)
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v must be 3-D (tokens, heads, head_dim) and of one shape")
+    T, Hkv, d = k.shape
+    dev = k.device
+    c = _cache_struct(cache, d, dev)
+    if c.Hkv != Hkv:
+        raise ValueError(f"the cache has {c.Hkv} heads, k {Hkv}")
+    _check_ints("page_table", page_table, (None, None), dev)
+    B = page_table.shape[0]
+    _check_ints("seq_lens", seq_lens, (B,), dev)
+    if cu_seqlens is not None:
+        _check_ints("cu_seqlens", cu_seqlens, (B + 1,), dev)
+    elif T != B:
+        raise ValueError(f"{T} tokens for {B} sequences: pass cu_seqlens")
+    _check_k_mean(k_mean, Hkv, d, dev)
+    Hq, qs, qos = 0, (0, 0), (0, 0)
+    if q is not None:
+        _check_heads("q", q, k)
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
+            raise ValueError(f"q of shape {tuple(q.shape)} does not fit k of shape {tuple(k.shape)}")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        _check_out("q_out", q_out, q.shape, q)
+        Hq, qs, qos = q.shape[1], (q.stride(0), q.stride(1)), (q_out.stride(0), q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    nr = _norm_rope(d, dev, norm, eps, q_weight, k_weight, cos_sin, interleaved)
+    strides = (ctypes.c_longlong * 8)(*qs, k.stride(0), k.stride(1), v.stride(0), v.stride(1), *qos)
+    _call(dev, "sage_cache_append", ctypes.byref(c), _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), strides,
+          page_table.data_ptr(), page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(), _ptr(cu_seqlens),
+          _ptr(k_mean), T, B, Hq, _DTYPES[k.dtype], ctypes.byref(nr))
+    return q_out
+
+
+def sage_cache_gather(cache, page_table, cu_seqlens, total, head_dim, dtype=torch.float16, starts=None, k_mean=None,
+                      k_out=None, v_out=None):
+    """Reads cached tokens back as (k, v), each (total, Hkv, head_dim) of ``dtype``: token i of sequence b (rows
+    cu_seqlens[b] .. cu_seqlens[b+1]-1) is position starts[b] + i (starts None: 0).  k_mean is added to the keys.
+    Rows behind the last sequence, and rows of bad pages, are left unwritten."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    dev = cache["k8"].device
+    c = _cache_struct(cache, head_dim, dev)
+    _check_ints("page_table", page_table, (None, None), dev)
+    B = page_table.shape[0]
+    _check_ints("cu_seqlens", cu_seqlens, (B + 1,), dev)
+    if starts is not None:
+        _check_ints("starts", starts, (B,), dev)
+    _check_k_mean(k_mean, c.Hkv, head_dim, dev)
+    shape = (int(total), c.Hkv, head_dim)
+    outs = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        if not (t.is_cuda and t.device == dev and t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
+        outs.append(t)
+    _call(dev, "sage_cache_gather", ctypes.byref(c), page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+          cu_seqlens.data_ptr(), _ptr(starts), _ptr(k_mean), outs[0].data_ptr(), outs[1].data_ptr(), shape[0], B,
+          _DTYPES[dtype])
+    return outs[0], outs[1]
+
+
+def sage_attn_decode(q, cache, page_table, seq_lens, max_seqlen, sm_scale=None, out=None):
+    """Attention of one new token per sequence, q (B,Hq,d), over its cached tokens: out (B,Hq,d).
+
+    seq_lens int32 (B,): the cached keys each query sees (0: zeros); max_seqlen bounds them (a longer sequence gets
+    zeros and is reported by sage_check_status).  q may be strided (channels contiguous)."""
+    _check_heads("q", q)
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D (sequences, heads, head_dim)")
+    B, Hq, d = q.shape
+    c = _cache_struct(cache, d, q.device)
+    _check_ints("page_table", page_table, (B, None), q.device)
+    _check_ints("seq_lens", seq_lens, (B,), q.device)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _check_out("out", out, q.shape, q)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    _call(q.device, "sage_attn_decode", q.data_ptr(), q.stride(0), q.stride(1), ctypes.byref(c), page_table.data_ptr(),
+          page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(), out.data_ptr(), B, Hq, int(max_seqlen),
+          _DTYPES[q.dtype], float(sm_scale) if sm_scale is not None else 0.0)
     return out
 
 

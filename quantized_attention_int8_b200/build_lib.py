@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsage_b200.so")
 LIB_CHECKED = os.path.join(PKG, "libsage_b200_checked.so")
-SOURCES = ["api.cu", "attn.cu", "quant.cu"]
+SOURCES = ["api.cu", "attn.cu", "quant.cu", "cache.cu", "decode.cu"]
 HEADERS = ["sm100.cuh", "sage_internal.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

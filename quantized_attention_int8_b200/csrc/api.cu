@@ -1,8 +1,10 @@
 // C ABI: argument checks, workspace, TMA tensor maps and launches.
 // The operation and the argument contract are documented in include/sage.h.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <atomic>
 #include <mutex>
 
@@ -576,7 +578,10 @@ sage_status sage_check_status(void* stream) {
   int qflags = 0;
   if (read_clear_device_error(&flags) != cudaSuccess) return SAGE_ERR_CUDA;
   if (read_clear_quant_error(&qflags) != cudaSuccess) return SAGE_ERR_CUDA;
-  flags |= qflags;
+  int cflags = 0, dflags = 0;
+  if (read_clear_cache_error(&cflags) != cudaSuccess) return SAGE_ERR_CUDA;
+  if (read_clear_decode_error(&dflags) != cudaSuccess) return SAGE_ERR_CUDA;
+  flags |= qflags | cflags | dflags;
   if (flags & 1) return SAGE_ERR_TIMEOUT;
   if (flags & SAGE_DEVERR_BOUNDS) return SAGE_ERR_BOUNDS;
   if (flags & 2) return SAGE_ERR_INVALID_ARG;
@@ -612,6 +617,270 @@ int sage_checked_build(void) {
 #else
   return 0;
 #endif
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------------
+// Serving: head norm and rotation, the paged cache, one-token attention.
+// ------------------------------------------------------------------------------------------------
+namespace {
+
+// Strides, and every view's extent along each dimension, stay below these, so that no offset passes 2^63.
+constexpr long long kMaxStride = 1LL << 40, kMaxExtent = 1LL << 48;
+constexpr long long kMaxItems = (1LL << 31) - 1;  // row groups of one launch (32-bit item numbers)
+
+sage_status check_strides(const long long* s, int n) {
+  if (!s) return SAGE_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (s[i] < 0 || s[i] > kMaxStride) return SAGE_ERR_INVALID_ARG;
+  return SAGE_OK;
+}
+
+sage_status check_norm_rope(const sage_norm_rope* nr, int d) {
+  if (!nr) return SAGE_ERR_INVALID_ARG;
+  if (nr->norm && !(nr->eps >= 0.f && nr->eps <= 3.4e38f)) return SAGE_ERR_INVALID_ARG;
+  if (nr->norm && (nr->q_weight || nr->k_weight)) {
+    if (nr->weight_dtype != SAGE_FP16 && nr->weight_dtype != SAGE_BF16 && nr->weight_dtype != SAGE_FP32)
+      return SAGE_ERR_INVALID_ARG;
+    const uintptr_t a = nr->weight_dtype == SAGE_FP32 ? 3 : 1;
+    if (((uintptr_t)nr->q_weight & a) || ((uintptr_t)nr->k_weight & a)) return SAGE_ERR_INVALID_ARG;
+  }
+  if (!nr->norm && (nr->q_weight || nr->k_weight)) return SAGE_ERR_INVALID_ARG;
+  if (nr->cos_sin) {
+    if (nr->n_pos < 1 || nr->rot < 2 || nr->rot > d || nr->rot % 2 != 0) return SAGE_ERR_INVALID_ARG;
+    if ((uintptr_t)nr->cos_sin & 3) return SAGE_ERR_INVALID_ARG;
+  }
+  return SAGE_OK;
+}
+
+sage_status check_cache(const sage_kv_cache* c, const int32_t* table, long long table_stride, int max_pages, int B,
+                        PageMap* m) {
+  if (!c || !c->k8 || !c->ks || !c->v8 || !c->vs) return SAGE_ERR_INVALID_ARG;
+  if (!aligned16(c->k8) || !aligned16(c->v8) || ((uintptr_t)c->ks & 3) || ((uintptr_t)c->vs & 3) ||
+      ((uintptr_t)table & 3))
+    return SAGE_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->Hkv < 1 || c->Hkv > 65535 || c->d < 1 || c->d > 256) return SAGE_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return SAGE_ERR_INVALID_ARG;
+  if (max_pages < 0 || table_stride < 0 || table_stride > kMaxStride) return SAGE_ERR_INVALID_ARG;
+  if (B > 0 && (!table || max_pages < 1)) return SAGE_ERR_INVALID_ARG;
+  if (B > 1 && table_stride < max_pages) return SAGE_ERR_INVALID_ARG;
+  m->k8 = c->k8, m->ks = c->ks, m->v8 = c->v8, m->vs = c->vs;
+  m->table = table, m->table_stride = table_stride;
+  m->max_pages = max_pages, m->num_pages = c->num_pages, m->Hkv = c->Hkv;
+  m->dc = (c->d + 15) / 16 * 16;
+  m->page_log2 = 0;
+  while ((1 << m->page_log2) < c->page_size) ++m->page_log2;
+  return SAGE_OK;
+}
+
+size_t cache_rows(const PageMap& m) { return ((size_t)m.num_pages * m.Hkv) << m.page_log2; }
+
+bool view_fits(const HeadView& v, long long B, long long N, long long H) {
+  const auto fits = [](long long n, long long stride) { return stride == 0 || (n - 1) <= kMaxExtent / stride; };
+  return fits(B, v.batch) && fits(N, v.token) && fits(H, v.head);
+}
+
+// Bytes from the first to behind the last element of (B, N, H, d) 16-bit values with these strides.
+size_t view_bytes(const HeadView& v, long long B, long long N, long long H, long long d) {
+  return (size_t)((B - 1) * v.batch + (N - 1) * v.token + (H - 1) * v.head + d) * 2;
+}
+
+// 16-byte vectors: the base aligned and every stride in use a multiple of eight elements.
+bool vec_view(const HeadView& v, long long B, long long N, long long H) {
+  return aligned16(v.ptr) && (B == 1 || v.batch % 8 == 0) && (N == 1 || v.token % 8 == 0) &&
+         (H == 1 || v.head % 8 == 0);
+}
+
+void set_norm_rope(HeadRowsParams* p, const sage_norm_rope& nr) {
+  p->norm = nr.norm ? 1 : 0, p->eps = nr.eps, p->inv_d = 1.0f / (float)p->d;
+  p->q_weight = nr.q_weight, p->k_weight = nr.k_weight, p->weight_dtype = nr.weight_dtype;
+  p->vec_weight = p->d % 8 == 0 && aligned16(nr.q_weight) && aligned16(nr.k_weight);
+  p->cos_sin = nr.cos_sin, p->n_pos = nr.n_pos, p->rot = nr.cos_sin ? nr.rot : 0, p->interleaved = nr.interleaved ? 1 : 0;
+  // a lane's eight channels lie in one half of the rotated ones, and its table entries in 16-byte vectors
+  if (nr.cos_sin && !nr.interleaved) p->vec = p->vec && nr.rot % 16 == 0 && aligned16(nr.cos_sin);
+}
+
+// Launch shape: groups take four heads of a token where that still gives every SM its full 2048
+// threads, else one.
+sage_status shape_rows(HeadRowsParams* p, int batches, int kinds_kv) {
+  const int lanes = p->d <= 64 ? 8 : p->d <= 128 ? 16 : 32;
+  const long long tokens = (long long)batches * p->N;
+  if (tokens > kMaxItems) return SAGE_ERR_INVALID_ARG;
+  const auto chunks = [&](int hc) {
+    p->q_chunks = (p->Hq + hc - 1) / hc, p->k_chunks = (p->Hkv + hc - 1) / hc;
+    p->chunks = p->q_chunks + kinds_kv * p->k_chunks;
+    return tokens * p->chunks;
+  };
+  p->heads_per_group = p->vec && chunks(4) * lanes >= 148LL * 2048 ? 4 : 1;
+  p->items = chunks(p->heads_per_group);
+  return p->items > kMaxItems ? SAGE_ERR_INVALID_ARG : SAGE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sage_status sage_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+                              const int32_t* positions, long long pos_batch_stride, int B, int N, int Hq, int Hkv,
+                              int d, sage_dtype dtype, const sage_norm_rope* nr, void* stream) {
+  sage_status s = check_dtype(dtype);
+  if (s != SAGE_OK) return s;
+  if (B < 0 || N < 0 || Hq < 1 || Hq > 65535 || d < 1 || d > 256) return SAGE_ERR_INVALID_ARG;
+  if (k && (Hkv < 1 || Hkv > 65535)) return SAGE_ERR_INVALID_ARG;
+  if ((s = check_strides(strides, 12)) != SAGE_OK) return s;
+  if ((s = check_norm_rope(nr, d)) != SAGE_OK) return s;
+  if (pos_batch_stride < 0 || pos_batch_stride > kMaxStride || ((uintptr_t)positions & 3)) return SAGE_ERR_INVALID_ARG;
+  if (B == 0 || N == 0) return SAGE_OK;
+  if (!q || !q_out || (k && !k_out)) return SAGE_ERR_INVALID_ARG;
+  if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)q_out | (uintptr_t)k_out) & 1) return SAGE_ERR_INVALID_ARG;
+  HeadRowsParams p;
+  memset(&p, 0, sizeof(p));
+  p.B = B, p.N = N, p.Hq = Hq, p.Hkv = k ? Hkv : 0, p.d = d;
+  p.q = HeadView{q, strides[0], strides[1], strides[2]};
+  p.k = HeadView{k, strides[3], strides[4], strides[5]};
+  p.q_out = HeadView{q_out, strides[6], strides[7], strides[8]};
+  p.k_out = HeadView{k_out, strides[9], strides[10], strides[11]};
+  if (!view_fits(p.q, B, N, Hq) || !view_fits(p.q_out, B, N, Hq) ||
+      (k && (!view_fits(p.k, B, N, Hkv) || !view_fits(p.k_out, B, N, Hkv))))
+    return SAGE_ERR_INVALID_ARG;
+  p.positions = positions, p.pos_batch = pos_batch_stride;
+  p.vec = d % 8 == 0 && vec_view(p.q, B, N, Hq) && vec_view(p.q_out, B, N, Hq) &&
+          (!k || (vec_view(p.k, B, N, Hkv) && vec_view(p.k_out, B, N, Hkv)));
+  set_norm_rope(&p, *nr);
+  p.token_fast = p.q.token < p.q.head;
+  p.x_q_out = extent_of(q_out, view_bytes(p.q_out, B, N, Hq, d));
+  if (k) p.x_k_out = extent_of(k_out, view_bytes(p.k_out, B, N, Hkv, d));
+  if ((s = shape_rows(&p, B, 1)) != SAGE_OK) return s;
+  if ((s = check_device()) != SAGE_OK) return s;
+  return from_cuda(launch_head_rows(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+sage_status sage_cache_append(const sage_kv_cache* cache, const void* q, const void* k, const void* v, void* q_out,
+                              const long long* strides, const int32_t* page_table, long long table_stride,
+                              int max_pages, const int32_t* seq_lens, const int32_t* cu_seqlens, const float* k_mean,
+                              int T, int B, int Hq, sage_dtype dtype, const sage_norm_rope* nr, void* stream) {
+  sage_status s = check_dtype(dtype);
+  if (s != SAGE_OK) return s;
+  HeadRowsParams p;
+  memset(&p, 0, sizeof(p));
+  if (T < 0 || B < 0 || (!cu_seqlens && T != B)) return SAGE_ERR_INVALID_ARG;
+  if ((s = check_strides(strides, 8)) != SAGE_OK) return s;
+  if ((s = check_cache(cache, page_table, table_stride, max_pages, B, &p.map)) != SAGE_OK) return s;
+  if (q && (!nr || Hq < 1 || Hq > 65535)) return SAGE_ERR_INVALID_ARG;
+  if (nr && (s = check_norm_rope(nr, cache->d)) != SAGE_OK) return s;
+  if (((uintptr_t)k_mean | (uintptr_t)seq_lens | (uintptr_t)cu_seqlens) & 3) return SAGE_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return SAGE_OK;
+  if (!k || !v || !seq_lens || (q && !q_out)) return SAGE_ERR_INVALID_ARG;
+  if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out) & 1) return SAGE_ERR_INVALID_ARG;
+  const int d = cache->d, Hkv = cache->Hkv;
+  p.B = B, p.N = T, p.Hq = q ? Hq : 0, p.Hkv = Hkv, p.d = d;
+  p.q = HeadView{q, 0, strides[0], strides[1]};
+  p.k = HeadView{k, 0, strides[2], strides[3]};
+  p.v = HeadView{v, 0, strides[4], strides[5]};
+  p.q_out = HeadView{q_out, 0, strides[6], strides[7]};
+  if (!view_fits(p.k, 1, T, Hkv) || !view_fits(p.v, 1, T, Hkv) ||
+      (q && (!view_fits(p.q, 1, T, Hq) || !view_fits(p.q_out, 1, T, Hq))))
+    return SAGE_ERR_INVALID_ARG;
+  p.append = 1, p.cu = cu_seqlens, p.seq_lens = seq_lens, p.k_mean = k_mean;
+  p.vec = d % 8 == 0 && vec_view(p.k, 1, T, Hkv) && vec_view(p.v, 1, T, Hkv) &&
+          (!q || (vec_view(p.q, 1, T, Hq) && vec_view(p.q_out, 1, T, Hq)));
+  p.vec_mean = d % 8 == 0 && aligned16(k_mean);
+  if (nr) set_norm_rope(&p, *nr);
+  if (q) p.x_q_out = extent_of(q_out, view_bytes(p.q_out, 1, T, Hq, d));
+  const size_t rows = cache_rows(p.map);
+  p.x_k8 = extent_of(cache->k8, rows * p.map.dc), p.x_v8 = extent_of(cache->v8, rows * p.map.dc);
+  p.x_ks = extent_of(cache->ks, rows * 4), p.x_vs = extent_of(cache->vs, rows * 4);
+  if ((s = shape_rows(&p, 1, 2)) != SAGE_OK) return s;
+  if ((s = check_device()) != SAGE_OK) return s;
+  return from_cuda(launch_head_rows(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+sage_status sage_cache_gather(const sage_kv_cache* cache, const int32_t* page_table, long long table_stride,
+                              int max_pages, const int32_t* cu_seqlens, const int32_t* starts, const float* k_mean,
+                              void* k_out, void* v_out, int T, int B, sage_dtype dtype, void* stream) {
+  sage_status s = check_dtype(dtype);
+  if (s != SAGE_OK) return s;
+  GatherParams p;
+  memset(&p, 0, sizeof(p));
+  if (T < 0 || B < 0) return SAGE_ERR_INVALID_ARG;
+  if ((s = check_cache(cache, page_table, table_stride, max_pages, B, &p.map)) != SAGE_OK) return s;
+  if (((uintptr_t)k_mean | (uintptr_t)starts | (uintptr_t)cu_seqlens) & 3) return SAGE_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return SAGE_OK;
+  if (!cu_seqlens || !k_out || !v_out || (((uintptr_t)k_out | (uintptr_t)v_out) & 1)) return SAGE_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)T * cache->Hkv * cache->d * 2, codes = cache_rows(p.map) * p.map.dc;
+  const size_t scales = cache_rows(p.map) * 4;
+  if (overlaps(k_out, bytes, v_out, bytes)) return SAGE_ERR_INVALID_ARG;
+  for (const void* o : {(const void*)k_out, (const void*)v_out})
+    if (overlaps(o, bytes, cache->k8, codes) || overlaps(o, bytes, cache->v8, codes) ||
+        overlaps(o, bytes, cache->ks, scales) || overlaps(o, bytes, cache->vs, scales))
+      return SAGE_ERR_INVALID_ARG;
+  p.cu = cu_seqlens, p.starts = starts, p.k_mean = k_mean, p.k_out = k_out, p.v_out = v_out;
+  p.B = B, p.T = T, p.d = cache->d;
+  p.items = (long long)T * cache->Hkv;
+  if (p.items > kMaxItems) return SAGE_ERR_INVALID_ARG;
+  p.vec = cache->d % 8 == 0 && aligned16(k_out) && aligned16(v_out);
+  p.vec_mean = cache->d % 8 == 0 && aligned16(k_mean);
+  p.x_k_out = extent_of(k_out, bytes), p.x_v_out = extent_of(v_out, bytes);
+  if ((s = check_device()) != SAGE_OK) return s;
+  return from_cuda(launch_cache_gather(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long q_head_stride,
+                             const sage_kv_cache* cache, const int32_t* page_table, long long table_stride,
+                             int max_pages, const int32_t* seq_lens, void* out, int B, int Hq, int max_seqlen,
+                             sage_dtype dtype, float sm_scale, void* stream) {
+  sage_status s = check_dtype(dtype);
+  if (s != SAGE_OK) return s;
+  DecodeParams p;
+  memset(&p, 0, sizeof(p));
+  const long long strides[2] = {q_batch_stride, q_head_stride};
+  if ((s = check_strides(strides, 2)) != SAGE_OK) return s;
+  if (B < 0 || B > 65535 || Hq < 1 || Hq > 65535 || max_seqlen < 0) return SAGE_ERR_INVALID_ARG;
+  if ((s = check_cache(cache, page_table, table_stride, max_pages, B, &p.map)) != SAGE_OK) return s;
+  if (Hq % cache->Hkv != 0) return SAGE_ERR_INVALID_ARG;
+  if (B == 0) return SAGE_OK;
+  if (!q || !out || !seq_lens || (((uintptr_t)q | (uintptr_t)out) & 1) || ((uintptr_t)seq_lens & 3))
+    return SAGE_ERR_INVALID_ARG;
+  p.q = HeadView{q, q_batch_stride, 0, q_head_stride};
+  const size_t out_bytes = (size_t)B * Hq * cache->d * 2;
+  if (overlaps(out, out_bytes, q, view_bytes(p.q, B, 1, Hq, cache->d))) return SAGE_ERR_INVALID_ARG;
+  p.out = out, p.seq_lens = seq_lens;
+  p.B = B, p.Hq = Hq, p.G = Hq / cache->Hkv, p.d = cache->d;
+  p.tiles = (p.G + 7) / 8;
+  const long long pairs = (long long)B * cache->Hkv * p.tiles;  // CTAs per chunk of keys
+  if ((long long)cache->Hkv * p.tiles > 65535) return SAGE_ERR_INVALID_ARG;
+  const long long room = (long long)max_pages << p.map.page_log2;
+  p.max_len = (int)std::min<long long>(std::min<long long>(max_seqlen, room), 1 << 30);
+  // Chunks of keys: enough for every SM to hold its share of CTAs, and then, while they stay 1024 keys
+  // or longer, more of them, so that sequences of different lengths spread evenly.
+  const long long resident = 148 * 4;
+  long long n = std::max<long long>(1, std::max((resident + pairs - 1) / pairs,
+                                                std::min<long long>(p.max_len / 1024, 16 * resident / pairs)));
+  n = std::min<long long>(n, std::max(1, (p.max_len + 127) / 128));
+  p.chunk = (int)((std::max(p.max_len, 1) + n * 64 - 1) / (n * 64) * 64);
+  p.nsplit = std::max(1, (p.max_len + p.chunk - 1) / p.chunk);
+  p.scale_log2 = resolve_scale(sm_scale, p.d) * 1.4426950408889634f;
+  p.vec_q = p.d % 4 == 0 && ((uintptr_t)q & 7) == 0 && (B == 1 || q_batch_stride % 4 == 0) &&
+            (Hq == 1 || q_head_stride % 4 == 0);
+  p.x_out = extent_of(out, out_bytes);
+  if ((s = check_device()) != SAGE_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  unsigned char* ws = nullptr;
+  if (p.nsplit > 1) {
+    const size_t parts = (size_t)B * Hq * p.nsplit;
+    const size_t ml = align_up(parts * 8), total = ml + parts * p.d * 4;
+    const cudaError_t e = workspace_alloc(reinterpret_cast<void**>(&ws), total, st);
+    if (e != cudaSuccess) return from_cuda(e);
+    p.part_ml = reinterpret_cast<float*>(ws), p.part_o = reinterpret_cast<float*>(ws + ml);
+    p.x_part_ml = extent_of(p.part_ml, parts * 8), p.x_part_o = extent_of(p.part_o, parts * p.d * 4);
+  }
+  s = from_cuda(launch_decode(p, dtype, st));
+  if (ws) {
+    const cudaError_t ef = cudaFreeAsync(ws, st);
+    if (s == SAGE_OK && ef != cudaSuccess) s = from_cuda(ef);
+  }
+  return s;
 }
 
 }  // extern "C"

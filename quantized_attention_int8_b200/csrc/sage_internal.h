@@ -150,7 +150,86 @@ struct QkDumpParams {
   int B, Hq, Hkv, Np, nblk, G;
 };
 
+// The paged cache and a batch's page table, as the kernels address them.
+struct PageMap {
+  int8_t* k8;   // [num_pages][Hkv][page_size][dc]
+  float* ks;    // [num_pages][Hkv][page_size]
+  uint8_t* v8;  // like k8
+  float* vs;    // like ks
+  const int32_t* table;  // [B][max_pages], rows table_stride apart
+  long long table_stride;
+  int max_pages, num_pages, page_log2, Hkv, dc;
+  // Row of (page, kv head, position) in ks / vs; dc codes each in k8 / v8.  64 bits: a cache passes 2^31 codes.
+  __host__ __device__ long long row(int page, int h, int pos) const {
+    return (((long long)page * Hkv + h) << page_log2) + (pos & ((1 << page_log2) - 1));
+  }
+};
+
+// Heads of 16-bit values: element strides between batches, tokens and heads; channels contiguous.
+struct HeadView {
+  const void* ptr;
+  long long batch, token, head;
+};
+
+struct HeadRowsParams {
+  HeadView q, k, v, q_out, k_out;
+  int B, N, Hq, Hkv, d;  // append: N packed tokens of B sequences
+  const int32_t* positions;  // [B][N], rows pos_batch apart; nullptr: token n is at position n
+  long long pos_batch;
+  int norm, weight_dtype;
+  float eps, inv_d;
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;  // [n_pos][rot]: rot / 2 cosines, then as many sines; nullptr: no rotation
+  int n_pos, rot, interleaved;
+  // cache write
+  int append;
+  const int32_t* cu;        // [B + 1] offsets of the sequences' tokens; nullptr: one token each
+  const int32_t* seq_lens;  // [B] lengths with the new tokens
+  const float* k_mean;      // [Hkv][d] or nullptr
+  PageMap map;
+  // launch shape
+  int heads_per_group, q_chunks, k_chunks, chunks;
+  int token_fast;  // consecutive groups take consecutive tokens (else consecutive heads of one token)
+  long long items;
+  bool vec, vec_weight, vec_mean;
+  Extent x_q_out, x_k_out, x_k8, x_ks, x_v8, x_vs;
+};
+
+struct GatherParams {
+  PageMap map;
+  const int32_t* cu;      // [B + 1]
+  const int32_t* starts;  // [B] first position read, or nullptr (0)
+  const float* k_mean;
+  void* k_out;  // [tokens][Hkv][d]
+  void* v_out;
+  int B, T, d;
+  long long items;  // T x Hkv
+  bool vec, vec_mean;
+  Extent x_k_out, x_v_out;
+};
+
+struct DecodeParams {
+  PageMap map;
+  HeadView q;  // token stride unused
+  void* out;   // [B][Hq][d]
+  const int32_t* seq_lens;
+  int B, Hq, G, d;
+  int max_len;     // longest sequence the launch covers
+  int chunk;       // keys per CTA (a multiple of 64)
+  int nsplit;      // ceil(max_len / chunk)
+  int tiles;       // tiles of 8 query heads per kv head
+  float scale_log2;
+  float* part_o;   // [B][Hq][nsplit][d]   (nsplit > 1)
+  float* part_ml;  // [B][Hq][nsplit][2]: running max (log2 units) and sum
+  bool vec_q;
+  Extent x_out, x_part_o, x_part_ml;
+};
+
 cudaError_t launch_quantize(const QuantParams& p, cudaStream_t st);
+cudaError_t launch_head_rows(const HeadRowsParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_cache_gather(const GatherParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_decode(const DecodeParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams& p,
                        int dtype, int causal, int pv_mode, cudaStream_t st);
 // Packed batches: per-sequence table from the caller's cumulative lengths (validated on the device;
@@ -159,6 +238,8 @@ cudaError_t launch_seq_plan(const int32_t* cu_q, const int32_t* cu_k, int B, int
                             long long total_q, long long total_k, SeqDesc* seqs, cudaStream_t st);
 cudaError_t read_clear_device_error(int* value);
 cudaError_t read_clear_quant_error(int* value);  // the quantize kernels' error word (quant.cu)
+cudaError_t read_clear_cache_error(int* value);   // cache.cu
+cudaError_t read_clear_decode_error(int* value);  // decode.cu
 cudaError_t launch_wait_probe(long long budget_cycles, cudaStream_t st);
 // tcgen05.mma issue-rate probe: kind 0 = kind::i8, 1 = kind::f8f6f4, 2 = kind::f16; one CTA per SM.
 cudaError_t launch_mma_probe(int kind, int iters, int n_sm, cudaStream_t st);
