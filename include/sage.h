@@ -267,7 +267,7 @@ sage_status sage_qk_norm_rope(const void* q, const void* k, void* q_out, void* k
                               int d, sage_dtype dtype, const sage_norm_rope* nr, void* stream);
 
 /* A paged cache of quantized K and V, device memory of the caller.  dc = 16 * ceil(d / 16); channels
- * d .. dc-1 hold code 0.  page_size is a power of two, 16 .. 1024.  k8, v8 16-byte aligned.
+ * d .. dc-1 hold code 0.  page_size is a power of two, 16 .. 1024.  All four arrays are 16-byte aligned.
  *   k8  int8   [num_pages][Hkv][page_size][dc]      ks  fp32 [num_pages][Hkv][page_size]
  *   v8  E4M3   [num_pages][Hkv][page_size][dc]      vs  fp32 [num_pages][Hkv][page_size]
  * A page table is DEVICE int32 [B][max_pages], rows table_stride elements apart: position p of sequence b is in

@@ -657,8 +657,7 @@ sage_status check_norm_rope(const sage_norm_rope* nr, int d) {
 sage_status check_cache(const sage_kv_cache* c, const int32_t* table, long long table_stride, int max_pages, int B,
                         PageMap* m) {
   if (!c || !c->k8 || !c->ks || !c->v8 || !c->vs) return SAGE_ERR_INVALID_ARG;
-  if (!aligned16(c->k8) || !aligned16(c->v8) || ((uintptr_t)c->ks & 3) || ((uintptr_t)c->vs & 3) ||
-      ((uintptr_t)table & 3))
+  if (!aligned16(c->k8) || !aligned16(c->v8) || !aligned16(c->ks) || !aligned16(c->vs) || ((uintptr_t)table & 3))
     return SAGE_ERR_INVALID_ARG;
   if (c->num_pages < 1 || c->Hkv < 1 || c->Hkv > 65535 || c->d < 1 || c->d > 256) return SAGE_ERR_INVALID_ARG;
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return SAGE_ERR_INVALID_ARG;
@@ -847,33 +846,30 @@ sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long 
   if (overlaps(out, out_bytes, q, view_bytes(p.q, B, 1, Hq, cache->d))) return SAGE_ERR_INVALID_ARG;
   p.out = out, p.seq_lens = seq_lens;
   p.B = B, p.Hq = Hq, p.G = Hq / cache->Hkv, p.d = cache->d;
-  p.tiles = (p.G + 7) / 8;
-  const long long pairs = (long long)B * cache->Hkv * p.tiles;  // CTAs per chunk of keys
-  if ((long long)cache->Hkv * p.tiles > 65535) return SAGE_ERR_INVALID_ARG;
+  p.tiles = (p.G + kDecodeHeads - 1) / kDecodeHeads;
+  p.pairs = cache->Hkv * p.tiles;
   const long long room = (long long)max_pages << p.map.page_log2;
   p.max_len = (int)std::min<long long>(std::min<long long>(max_seqlen, room), 1 << 30);
-  // Chunks of keys: enough for every SM to hold its share of CTAs, and then, while they stay 1024 keys
-  // or longer, more of them, so that sequences of different lengths spread evenly.
-  const long long resident = 148 * 4;
-  long long n = std::max<long long>(1, std::max((resident + pairs - 1) / pairs,
-                                                std::min<long long>(p.max_len / 1024, 16 * resident / pairs)));
-  n = std::min<long long>(n, std::max(1, (p.max_len + 127) / 128));
-  p.chunk = (int)((std::max(p.max_len, 1) + n * 64 - 1) / (n * 64) * 64);
-  p.nsplit = std::max(1, (p.max_len + p.chunk - 1) / p.chunk);
   p.scale_log2 = resolve_scale(sm_scale, p.d) * 1.4426950408889634f;
-  p.vec_q = p.d % 4 == 0 && ((uintptr_t)q & 7) == 0 && (B == 1 || q_batch_stride % 4 == 0) &&
-            (Hq == 1 || q_head_stride % 4 == 0);
   p.x_out = extent_of(out, out_bytes);
   if ((s = check_device()) != SAGE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // one CTA per unit of work, but no more than run at the same time on a B200's 148 SMs
+  const auto units = [&] {
+    return (long long)B * p.pairs * std::max<long long>(1, ((long long)p.max_len + (1 << p.unit_log2) - 1) >> p.unit_log2);
+  };
+  p.unit_log2 = 6;
+  while (units() >= (1LL << 31) && p.unit_log2 < 30) ++p.unit_log2;
+  if (units() >= (1LL << 31)) return SAGE_ERR_INVALID_ARG;
+  p.ctas = (uint32_t)std::min<long long>(units(), 148LL * decode_ctas_per_sm(p.d));
   unsigned char* ws = nullptr;
-  if (p.nsplit > 1) {
-    const size_t parts = (size_t)B * Hq * p.nsplit;
-    const size_t ml = align_up(parts * 8), total = ml + parts * p.d * 4;
+  if (p.max_len > 1 << p.unit_log2) {  // a pair may cross CTAs
+    const size_t parts = (size_t)p.ctas * 2 * kDecodeHeads;
+    const size_t ml = align_up(parts * 8), total = ml + parts * p.map.dc * 4;
     const cudaError_t e = workspace_alloc(reinterpret_cast<void**>(&ws), total, st);
     if (e != cudaSuccess) return from_cuda(e);
     p.part_ml = reinterpret_cast<float*>(ws), p.part_o = reinterpret_cast<float*>(ws + ml);
-    p.x_part_ml = extent_of(p.part_ml, parts * 8), p.x_part_o = extent_of(p.part_o, parts * p.d * 4);
+    p.x_part_ml = extent_of(p.part_ml, parts * 8), p.x_part_o = extent_of(p.part_o, parts * p.map.dc * 4);
   }
   s = from_cuda(launch_decode(p, dtype, st));
   if (ws) {

@@ -10,12 +10,18 @@
 // Keys are the M rows of both products, query heads the N columns (tiles of 8):
 //   S^T = K Q^T       m16n8k16, A = 16 keys x 16 channels, codes widened exactly to the type of q
 //   O^T = V^T P^T     m16n8k16, A = 16 channels x 16 keys, E4M3 widened exactly to fp16
-// A handful of query rows cannot fill a 128-row tcgen05 tile, and the tensor work is a few percent of
-// the time here; what counts is that no operand needs a detour through shared memory:
+// A handful of query rows cannot fill a 128-row tcgen05 tile, and the tensor work is a sixth of the
+// time here.  What counts is that the codes arrive at the rate of HBM, and get from shared memory
+// into the products with few instructions:
+//   * bulk copies, one elected lane to a run of rows: 2 KB of K, 512 bytes of V.  16-byte copies by the
+//     lanes that use them (no bank conflicts, no barrier) reached 4.2 TB/s on B32 L16384 Hq32 Hkv8 d128, with
+//     the arithmetic left out; bulk copies 6.3 TB/s;
 //   * the channels of a k16 step may be any 16, as long as K and Q agree, so a lane's 16 contiguous
 //     bytes of a K row serve four steps;
 //   * a lane's 16 contiguous channels of four V rows are paired by key with byte permutes, and give
-//     eight A tiles;
+//     eight A tiles.  Row i of S is key 4 (i / 2) + i % 2 for i < 8 and two keys on for i + 8, so that lane t's
+//     keys are the four rows 4 t ..; those groups of four are 32 bytes apart from one another's
+//     banks, and the reads have no conflicts (K's have two-way ones);
 //   * the scores' C layout becomes P^T's B layout by one 8x8 transpose (movmatrix) per 8 keys.
 //
 // V's scale is folded into the weights: w_j = s_j + log2(vs_j) has a running reference of its own, so
@@ -44,8 +50,8 @@ cudaError_t read_clear_decode_error(int* value) {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kHeads = 8;       // query heads per tile (N of the products)
-constexpr int kBadArg = 2;      // the error word's bit for SAGE_ERR_INVALID_ARG
+constexpr int kHeads = kDecodeHeads;  // query heads per tile (N of the products)
+constexpr int kTimeout = 1, kBadArg = 2;  // the error word's bits for SAGE_ERR_TIMEOUT and SAGE_ERR_INVALID_ARG
 constexpr float kLag = 8.f;     // the reference moves when a score passes it by 2^8: a weight stays below 2^8 in fp16
 
 __device__ __forceinline__ float ex2(float x) {
@@ -59,23 +65,11 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-template <typename T>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma16816<__half>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                 uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 8x8 transpose of 16-bit values spread over the warp (two per lane).
@@ -85,38 +79,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// Two INT8 codes of a word (bytes 0, 1 or 2, 3) widened exactly.
-// fp16: the byte as code + 128 in the low mantissa bits of 1024, less 1152.
-// bf16 has 7 mantissa bits: the low seven bits in those of 128, less 128, or 256 where the sign bit is set.
-template <typename T, int PAIR>
-__device__ __forceinline__ uint32_t widen_int8(uint32_t word);
-template <>
-__device__ __forceinline__ uint32_t widen_int8<__half, 0>(uint32_t word) {
-  const uint32_t h = __byte_perm(word ^ 0x80808080u, 0x64646464u, 0x4140);
-  const uint32_t bias = 0x64806480u;
+// Two INT8 codes of a word whose sign bits were flipped (bytes picked by `sel`), widened exactly to fp16:
+// each byte, now code + 128, goes to the low mantissa bits of 1024; less 1152.
+__device__ __forceinline__ uint32_t widen_int8(uint32_t flipped, uint32_t sel) {
+  const uint32_t h = __byte_perm(flipped, 0x64646464u, sel), bias = 0x64806480u;
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&bias));
   return *reinterpret_cast<const uint32_t*>(&r);
-}
-template <>
-__device__ __forceinline__ uint32_t widen_int8<__half, 1>(uint32_t word) {
-  const uint32_t h = __byte_perm(word ^ 0x80808080u, 0x64646464u, 0x4342);
-  const uint32_t bias = 0x64806480u;
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&bias));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t widen_bf16_bits(uint32_t h) {
-  const uint32_t low = h & 0xFF7FFF7Fu, bias = h & 0xFF80FF80u;
-  const __nv_bfloat162 r =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&low), *reinterpret_cast<const __nv_bfloat162*>(&bias));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-template <>
-__device__ __forceinline__ uint32_t widen_int8<__nv_bfloat16, 0>(uint32_t word) {
-  return widen_bf16_bits(__byte_perm(word, 0x43434343u, 0x4140));
-}
-template <>
-__device__ __forceinline__ uint32_t widen_int8<__nv_bfloat16, 1>(uint32_t word) {
-  return widen_bf16_bits(__byte_perm(word, 0x43434343u, 0x4342));
 }
 
 __device__ __forceinline__ uint32_t widen_e4m3(uint32_t pair16) {
@@ -129,6 +97,67 @@ __device__ __forceinline__ float max_over_keys(float v) {
   for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// Copy of `bytes` (a multiple of 16, both addresses 16-byte aligned), counted on an mbarrier.
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void barrier_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits for the phase with this parity; gives up after about a second (never seen: the copies are
+// this warp's own) and reports it.
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity) {
+  long long t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000)
+        : "memory");
+    if (ok) return true;
+    if (t0 == 0) t0 = clock64();
+    if (clock64() - t0 > 2000000000LL) {
+      atomicOr(&g_decode_error, kTimeout);
+      return false;
+    }
+  }
+}
+
+// One warp's ring of stages in shared memory, kTiles 16-key tiles to a stage.  A tile: 16 K rows; four groups of
+// four V rows, kPad bytes apart; 16 K scales and 16 V scales.  Two tiles are worked on at a time where they
+// fit: the chain from a score to its weight is latency, and three warps to a scheduler hide little of it.
+template <int DP>
+struct Ring {
+  static constexpr int kTiles = DP == 256 ? 1 : 2;
+  static constexpr int kStages = DP == 128 ? 2 : 3;
+  static constexpr int kPad = 32;
+  static __host__ __device__ constexpr int v_at(int dc) { return 16 * dc; }
+  static __host__ __device__ constexpr int v_group(int dc) { return 4 * dc + kPad; }
+  static __host__ __device__ constexpr int scales_at(int dc) { return 32 * dc + 4 * kPad; }
+  static __host__ __device__ constexpr int tile_bytes(int dc) { return 32 * dc + 4 * kPad + 128; }
+  static __host__ __device__ constexpr int warp_bytes(int dc) { return kStages * kTiles * tile_bytes(dc); }
+  // The lanes of channels behind dc read past their rows (what they read is not used): DP bytes behind the
+  // last tile.  The warps' O takes the rings' place at the end.
+  static __host__ __device__ constexpr int cta_bytes(int dc) {
+    return kWarps * warp_bytes(dc) + DP > kWarps * kHeads * DP * 4 ? kWarps * warp_bytes(dc) + DP
+                                                                   : kWarps * kHeads * DP * 4;
+  }
+};
+
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
@@ -145,253 +174,497 @@ __device__ __forceinline__ int seq_len_of(const DecodeParams& p, int b, bool rep
   return 0;
 }
 
+// The work, cut into units of 64 keys (more where 2^31 of those would not do) of one (sequence, kv head, tile
+// of heads): sequence by sequence, its pairs of kv head and head tile one after the other.  Every CTA takes
+// the same number of units, whatever the sequences' lengths, so that a ragged batch ends everywhere at
+// once; a pair that crosses CTAs is joined.
+__device__ __forceinline__ uint32_t units_of(const DecodeParams& p, int len) {
+  return len > 0 ? ((uint32_t)(len - 1) >> p.unit_log2) + 1 : 1;  // an empty sequence: one, to write its zeros
+}
+
+struct Place {
+  uint32_t share;     // units per CTA
+  uint32_t total;     // units in all
+  uint32_t pair0;     // first unit of the pair at the searched unit
+  int b, pair, len;   // sequence (-1: behind the last unit), pair within it, its length
+};
+
+// Finds the pair that holds unit cta * share.  All NT threads of the CTA call it.
+template <int NT>
+__device__ __forceinline__ Place find_place(const DecodeParams& p, uint32_t cta, bool report) {
+  __shared__ uint32_t sm_sum[NT / 32];
+  __shared__ Place sm_place;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.B + NT - 1) / NT, b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+  uint32_t mine = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) mine += units_of(p, seq_len_of(p, b, report));
+  uint32_t before = mine;  // inclusive scan over the warp, then over the warps
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, before, x);
+    if (lane >= x) before += v;
+  }
+  if (lane == 31) sm_sum[warp] = before;
+  if (threadIdx.x == 0) sm_place.b = -1;
+  __syncthreads();
+  uint32_t total = 0;
+#pragma unroll
+  for (int x = 0; x < NT / 32; ++x) {
+    if (x < warp) before += sm_sum[x];
+    total += sm_sum[x];
+  }
+  before -= mine;
+  const uint32_t all = total * p.pairs, share = (all + p.ctas - 1) / p.ctas, u = cta * share;
+  if (u < all && before * p.pairs <= u && u < (before + mine) * p.pairs) {  // one thread
+    int b = b0, len;
+    uint32_t n;
+#pragma unroll 1
+    for (;; ++b, before += n) {
+      len = seq_len_of(p, b, false);
+      n = units_of(p, len);
+      if (b + 1 == b1 || u < (before + n) * p.pairs) break;
+    }
+    const uint32_t pair = (u - before * p.pairs) / n;
+    sm_place.b = b, sm_place.pair = (int)pair, sm_place.len = len, sm_place.pair0 = before * p.pairs + pair * n;
+  }
+  __syncthreads();
+  Place at = sm_place;
+  at.share = share, at.total = all;
+  return at;
+}
+
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams p) {
-  constexpr int KC = DP / 64;   // 16-byte pieces of a K row per lane
-  constexpr int VB = DP / 8;    // bytes (= channels) of a V row per lane
-  constexpr int VW = VB / 4;    // words of them
-  constexpr bool kSplitP = sizeof(T) == 2 && std::is_same<T, __half>::value;
-  __shared__ float sm_o[kWarps][kHeads][DP];
-  __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
+__global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(DecodeParams p) {
+  using R = Ring<DP>;
+  constexpr int KC = DP / 64;             // 16-byte pieces of a K row per lane
+  constexpr int VP = DP < 128 ? 8 : 16;   // bytes (= channels) of a V row that a lane reads at a time
+  constexpr int VC = DP / 8 / VP;         // and how often, 8 VP channels apart
+  constexpr int VW = VP / 4;              // words of them
+  constexpr bool kSplitP = std::is_same<T, __half>::value;
+  constexpr int QP = DP + 8;              // pitch of Q in shared memory
+  extern __shared__ __align__(128) unsigned char smem[];  // the warps' rings; later their O, [kWarps][kHeads][DP] floats
+  __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads], sm_hf[kHeads];
+  __shared__ __align__(16) __half sm_q[kHeads * QP];
+  __shared__ __align__(8) uint64_t sm_bar[kWarps][R::kStages];
+  __shared__ int sm_dead;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x, b = blockIdx.z;
-  const int hkv = blockIdx.y / p.tiles, head0 = (blockIdx.y % p.tiles) * kHeads;  // first head within the group
-  const int nheads = min(kHeads, p.G - head0);
-  const int len = seq_len_of(p, b, split == 0 && blockIdx.y == 0 && threadIdx.x == 0);
-  const int k0 = split * p.chunk, k1 = min(len, k0 + p.chunk);
-  if (k0 >= len && split > 0) return;
+  const int dc = p.map.dc, tile_bytes = R::tile_bytes(dc);
+  unsigned char* const ring = smem + warp * R::warp_bytes(dc);
+  const uint32_t bars = smem_addr(sm_bar[warp]);
+  if (threadIdx.x == 0) sm_dead = 0;
+  if (lane < R::kStages) barrier_init(bars + 8 * lane);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join takes the SMs that this grid frees
+  const Place at = find_place<kThreads>(p, blockIdx.x, blockIdx.x == 0);
+  if (at.b < 0) return;
+  uint32_t unit = blockIdx.x * at.share, pair0 = at.pair0, parity = 0;  // parity: bit per stage
+  const uint32_t unit_end = min(at.total, unit + at.share);
+  int b = at.b, pair = at.pair, len = at.len;
 
-  // ---- Q: B operand of S^T.  Step (c, i) of the channels takes from lane t the channels
-  // 64 c + 16 t + 4 i .. + 3 of head g.
-  uint32_t qf[KC * 4][2];
-  {
-    const unsigned short* q = static_cast<const unsigned short*>(p.q.ptr) + (long long)b * p.q.batch +
-                              (long long)(hkv * p.G + head0 + g) * p.q.head;
-#pragma unroll
-    for (int s = 0; s < KC * 4; ++s) {
-      const int c = 64 * (s >> 2) + 16 * t + 4 * (s & 3);
-      qf[s][0] = qf[s][1] = 0;
-      if (g < nheads) {
-        if (p.vec_q) {
-          if (c < p.d) {
-            const uint2 v = *reinterpret_cast<const uint2*>(q + c);
-            qf[s][0] = v.x, qf[s][1] = v.y;
+  while (true) {  // one segment: this CTA's keys of one pair
+    const uint32_t n_pair = units_of(p, len), rel = unit - pair0, n_seg = min(n_pair - rel, unit_end - unit);
+    const int hkv = pair / p.tiles, head0 = (pair % p.tiles) * kHeads;  // first head within the group
+    const int nheads = min(kHeads, p.G - head0);
+    const int k0 = (int)(rel << p.unit_log2);
+    const int k1 = n_seg == n_pair - rel ? len : (int)((rel + n_seg) << p.unit_log2);
+
+    // ---- this warp's run of 16-key tiles, each of one page (page sizes are multiples of 16)
+    const int ntiles = (k1 - k0 + 15) >> 4, per_warp = (ntiles + kWarps - 1) / kWarps;
+    const int tile0 = min(warp * per_warp, ntiles), n_mine = min(per_warp, ntiles - tile0);
+    const int j0 = k0 + 16 * tile0, j1 = min(k1, j0 + 16 * n_mine);
+    const int steps = (n_mine + R::kTiles - 1) / R::kTiles;
+    // Lanes 8 x .. 8 x + 6 copy tile x of a step: its K rows, four groups of V rows, the scales of each.
+    const int32_t* table = p.map.table + b * p.map.table_stride;
+    const int my_tile = lane >> 3, my_part = lane & 7;
+    const auto my_page = [&](int step) {
+      const int i = step * R::kTiles + my_tile;
+      return my_tile < R::kTiles && i < n_mine ? table[(j0 + 16 * i) >> p.map.page_log2] : -1;
+    };
+    int stage_in = 0, page = my_page(0);
+    uint32_t there = 0;  // bit x: the tile fetched x tiles ago was copied (exists, and not on a bad page)
+    const auto fetch_step = [&](int step) {
+      if (step < steps) {
+        const int i = step * R::kTiles + my_tile, j = j0 + 16 * i;
+        const bool mine = my_tile < R::kTiles && i < n_mine, good = (unsigned)page < (unsigned)p.map.num_pages;
+        if (mine && !good && my_part == 0) atomicOr(&g_decode_error, kBadArg);
+        const uint32_t copied = __ballot_sync(0xffffffffu, mine && good && my_part == 0);
+        const uint32_t bar = bars + 8 * stage_in;
+        if (lane == 0) barrier_expect(bar, __popc(copied) * (32 * dc + 128));
+        __syncwarp();
+        if (mine && good && my_part < 7) {
+          const long long row = p.map.row(page, hkv, j);
+          uint32_t dst = smem_addr(ring) + (stage_in * R::kTiles + my_tile) * tile_bytes, bytes = 16 * dc;
+          const void* src = p.map.k8 + row * dc;
+          if (my_part > 4) {
+            bytes = 64, src = (my_part == 5 ? p.map.ks : p.map.vs) + row, dst += R::scales_at(dc) + (my_part - 5) * 64;
+          } else if (my_part > 0) {
+            bytes = 4 * dc, src = p.map.v8 + (row + 4 * (my_part - 1)) * dc;
+            dst += R::v_at(dc) + (my_part - 1) * R::v_group(dc);
           }
-        } else {
+          copy_bulk(dst, src, bytes, bar);
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e < p.d) qf[s][e >> 1] |= (uint32_t)q[c + e] << (16 * (e & 1));
+        for (int x = 0; x < R::kTiles; ++x) there = there << 1 | (copied >> (8 * x) & 1);
+      } else {
+        there <<= R::kTiles;
+      }
+      stage_in = stage_in + 1 == R::kStages ? 0 : stage_in + 1;
+      page = my_page(step + 1);
+    };
+#pragma unroll 1
+    for (int i = 0; i < R::kStages - 1; ++i) fetch_step(i);
+
+    // ---- Q: B operand of S^T.  Step (c, i) of the channels takes from lane t the channels
+    // 64 c + 16 t + 4 i .. + 3 of head g.  As fp16 whatever its type: a bf16 head is scaled by the power of two that
+    // takes its largest value to 2^14 .. 2^15, which is exact down to 2^-29 of that value and rounds to
+    // 2^-40 of it below (fp32 sums are off by more).
+#pragma unroll 1
+    for (int head = warp; head < kHeads; head += kWarps) {
+      const T* q = static_cast<const T*>(p.q.ptr) + (long long)b * p.q.batch +
+                   (long long)(hkv * p.G + head0 + head) * p.q.head;
+      float x[DP / 32];
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < DP / 32; ++e) {
+        const int c = lane + 32 * e;
+        x[e] = head < nheads && c < p.d ? to_f32(q[c]) : 0.f;
+        top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+      }
+      float up = 1.f, hf = p.scale_log2;
+      if (!kSplitP) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        const int e = min(max(127 + 14 - (int)(top >> 23), -126), 126);
+        up = __uint_as_float((uint32_t)(127 + e) << 23), hf *= __uint_as_float((uint32_t)(127 - e) << 23);
+      }
+#pragma unroll
+      for (int e = 0; e < DP / 32; ++e) sm_q[head * QP + lane + 32 * e] = __float2half_rn(x[e] * up);
+      if (lane == 0) sm_hf[head] = hf;
+    }
+    __syncthreads();
+    uint2 qf[KC * 4];
+#pragma unroll
+    for (int s = 0; s < KC * 4; ++s)
+      qf[s] = *reinterpret_cast<const uint2*>(sm_q + g * QP + 64 * (s >> 2) + 16 * t + 4 * (s & 3));
+    const float hf[2] = {sm_hf[2 * t], sm_hf[2 * t + 1]};  // score factor of heads 2t and 2t + 1
+
+    float o[VC * VW * 2][4];  // O^T: tile (q VW + w) 2 + hh holds channels 8 VP q + VP g + 4 w + 2 hh, + 1 (rows g, g + 8) of heads 2t, 2t + 1
+#pragma unroll
+    for (int m = 0; m < VC * VW * 2; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[m][e] = 0.f;
+    float ms[2] = {-FLT_MAX, -FLT_MAX}, mw[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
+
+    const int krow = (4 * (g >> 1) + (g & 1));  // key of S's row g; two more for row g + 8
+    const unsigned char* const k_lane = ring + krow * dc + 16 * t;
+    const unsigned char* const v_lane = ring + R::v_at(dc) + t * R::v_group(dc) + VP * g;
+    int stage = 0;
+#pragma unroll 1
+    for (int it = 0; it < steps; ++it) {
+      const bool arrived = barrier_wait(bars + 8 * stage, parity >> stage & 1);
+      parity ^= 1u << stage;
+      if (!__all_sync(0xffffffffu, arrived)) {  // gave up: wind down, with the copies in flight given their time
+        for (int x = 1; x < R::kStages - 1 && it + x < steps; ++x) barrier_wait(bars + 8 * ((stage + x) % R::kStages),
+                                                                           parity >> (stage + x) % R::kStages & 1);
+        sm_dead = 1;
+        break;
+      }
+      // (past the vote: all lanes are done with the stage filled next)
+      fetch_step(it + R::kStages - 1);
+      const int at_stage = stage * R::kTiles * tile_bytes;
+      stage = stage + 1 == R::kStages ? 0 : stage + 1;
+
+      // Keys of each tile that count.  V rows behind them (whatever their page holds, or held before) become
+      // zeros: a weight of 0 times a NaN code would be a NaN.
+      int n[R::kTiles];
+#pragma unroll
+      for (int x = 0; x < R::kTiles; ++x) {
+        n[x] = there >> (R::kStages * R::kTiles - 1 - x) & 1 ? min(16, j1 - (j0 + 16 * (it * R::kTiles + x))) : 0;
+        if (n[x] < 16) {
+          unsigned char* v = ring + at_stage + x * tile_bytes + R::v_at(dc);
+#pragma unroll 1
+          for (int r = n[x] + (lane >> 3); r < 16; r += 4)
+#pragma unroll 1
+            for (int c = 16 * (lane & 7); c < dc; c += 128)
+              *reinterpret_cast<uint4*>(v + (r >> 2) * R::v_group(dc) + (r & 3) * dc + c) = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later copy into the stage
+          __syncwarp();
         }
       }
-    }
-  }
 
-  float o[VW * 2][4];  // O^T: tile m = 2 w + hh holds channels VB g + 4 w + 2 hh, + 1 (rows g, g + 8) of heads 2t, 2t + 1
+      float s[R::kTiles][4], w[R::kTiles][4];  // rows g (0, 1) and g + 8 (2, 3) of heads 2t and 2t + 1
 #pragma unroll
-  for (int m = 0; m < VW * 2; ++m)
+      for (int x = 0; x < R::kTiles; ++x)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[m][e] = 0.f;
-  float ms[2] = {-FLT_MAX, -FLT_MAX}, mw[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
-
-  for (int j = k0 + 16 * warp; j < k1; j += 16 * kWarps) {
-    // 16 keys, all of one page (page sizes are multiples of 16)
-    const int page = p.map.table[b * p.map.table_stride + (j >> p.map.page_log2)];
-    if ((unsigned)page >= (unsigned)p.map.num_pages) {
-      if (lane == 0) atomicOr(&g_decode_error, kBadArg);
-      continue;  // its keys are left out
-    }
-    const long long row = p.map.row(page, hkv, j);
-    const int n = min(16, k1 - j);  // rows behind the sequence are not read: they may hold anything
-    uint4 kc[2][KC];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
+        for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
-        const int ch = 64 * c + 16 * t;
-        kc[r][c] = make_uint4(0, 0, 0, 0);
-        if (g + 8 * r < n && ch < p.map.dc)
-          kc[r][c] = *reinterpret_cast<const uint4*>(p.map.k8 + (row + g + 8 * r) * p.map.dc + ch);
+        uint4 rows[R::kTiles][2];
+#pragma unroll
+        for (int x = 0; x < R::kTiles; ++x)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            rows[x][r] = *reinterpret_cast<const uint4*>(k_lane + at_stage + x * tile_bytes + 2 * r * dc + 64 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int x = 0; x < R::kTiles; ++x) {
+            const uint32_t w0 = (&rows[x][0].x)[i] ^ 0x80808080u, w1 = (&rows[x][1].x)[i] ^ 0x80808080u;
+            mma16816(s[x], widen_int8(w0, 0x4140), widen_int8(w1, 0x4140), widen_int8(w0, 0x4342),
+                     widen_int8(w1, 0x4342), qf[4 * c + i].x, qf[4 * c + i].y);
+          }
       }
-    uint32_t vc[4][VW];
+      bool move = false;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int key = 2 * t + (r & 1) + 8 * (r >> 1);
-      const bool in = key < n && VB * g < p.map.dc;
-      const uint8_t* src = p.map.v8 + (row + key) * p.map.dc + VB * g;
-      if (VB == 8) {
-        const uint2 v = in ? *reinterpret_cast<const uint2*>(src) : make_uint2(0, 0);
-        vc[r][0] = v.x, vc[r][1] = v.y;
+      for (int x = 0; x < R::kTiles; ++x) {
+        const float* scales = reinterpret_cast<const float*>(ring + at_stage + x * tile_bytes + R::scales_at(dc));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int key = krow + 2 * r;
+          const float kf = scales[key], lv = lg2(scales[16 + key]);
+          const bool in = key < n[x];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int e = 2 * r + h;
+            s[x][e] = in ? s[x][e] * hf[h] * kf : -INFINITY;
+            w[x][e] = in ? s[x][e] + lv : -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          move |= fmaxf(s[x][h], s[x][2 + h]) > ms[h] + kLag || fmaxf(w[x][h], w[x][2 + h]) > mw[h] + kLag;
+      }
+      if (__any_sync(0xffffffffu, move)) {
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float ts = fmaxf(s[0][h], s[0][2 + h]), tw = fmaxf(w[0][h], w[0][2 + h]);
+#pragma unroll
+          for (int x = 1; x < R::kTiles; ++x)
+            ts = fmaxf(ts, fmaxf(s[x][h], s[x][2 + h])), tw = fmaxf(tw, fmaxf(w[x][h], w[x][2 + h]));
+          const float nms = fmaxf(ms[h], max_over_keys(ts)), nmw = fmaxf(mw[h], max_over_keys(tw));
+          l[h] *= ex2(ms[h] - nms);
+          f[h] = ex2(mw[h] - nmw);
+          ms[h] = nms, mw[h] = nmw;
+        }
+#pragma unroll
+        for (int m = 0; m < VC * VW * 2; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[m][e] *= f[e & 1];
+      }
+      // P^T as B operand: fp16.  For fp16 outputs a second fp16 term carries what the first rounds off
+      // (2^-12 of a weight would be as large as the output's own rounding).
+      uint32_t ph[R::kTiles][2], pl[R::kTiles][2];
+#pragma unroll
+      for (int x = 0; x < R::kTiles; ++x) {
+        float pw[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          l[e & 1] += ex2(s[x][e] - ms[e & 1]);
+          pw[e] = ex2(w[x][e] - mw[e & 1]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const __half2 hi = __floats2half2_rn(pw[2 * r], pw[2 * r + 1]);
+          ph[x][r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
+          if (kSplitP) {
+            const float2 back = __half22float2(hi);
+            const __half2 lo = __floats2half2_rn(pw[2 * r] - back.x, pw[2 * r + 1] - back.y);
+            pl[x][r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < R::kTiles; ++x)
+#pragma unroll
+        for (int q = 0; q < VC; ++q) {
+          uint32_t vc[4][VW];  // keys 4 t .. 4 t + 3
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const unsigned char* src = v_lane + at_stage + x * tile_bytes + r * dc + 8 * VP * q;
+            if (VP == 8) {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              vc[r][0] = v.x, vc[r][1] = v.y;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4*>(src);
+              vc[r][0] = v.x, vc[r][1] = v.y, vc[r][VW - 2] = v.z, vc[r][VW - 1] = v.w;
+            }
+          }
+#pragma unroll
+          for (int wd = 0; wd < VW; ++wd)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const uint32_t sel = hh ? 0x7362 : 0x5140;
+              const uint32_t x0 = __byte_perm(vc[0][wd], vc[1][wd], sel), x1 = __byte_perm(vc[2][wd], vc[3][wd], sel);
+              const uint32_t a0 = widen_e4m3(x0 & 0xFFFFu), a1 = widen_e4m3(x0 >> 16), a2 = widen_e4m3(x1 & 0xFFFFu),
+                             a3 = widen_e4m3(x1 >> 16);
+              float(&om)[4] = o[(q * VW + wd) * 2 + hh];
+              mma16816(om, a0, a1, a2, a3, ph[x][0], ph[x][1]);
+              if (kSplitP) mma16816(om, a0, a1, a2, a3, pl[x][0], pl[x][1]);
+            }
+        }
+    }
+
+    // ---- join the warps: O moves to the reference of the scores, then to the largest one
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+      if (g == 0) sm_m[warp][2 * t + h] = ms[h], sm_l[warp][2 * t + h] = l[h];
+    }
+    __syncthreads();  // and every warp is done with its ring
+    float* const sm_o = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int head = 2 * t + h;
+      float top = sm_m[0][head];
+#pragma unroll
+      for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm_m[x][head]);
+      const float f = ex2(mw[h] - top);
+#pragma unroll
+      for (int q = 0; q < VC; ++q)
+#pragma unroll
+        for (int m = 0; m < VW * 2; ++m) {
+          float* dst = sm_o + (warp * kHeads + head) * DP + 8 * VP * q + VP * g + 2 * m;
+          *reinterpret_cast<float2*>(dst) = make_float2(o[q * VW * 2 + m][h] * f, o[q * VW * 2 + m][2 + h] * f);
+        }
+    }
+    __syncthreads();
+    const bool whole = n_seg == n_pair;  // this CTA saw all of the pair's keys
+    const int part = blockIdx.x * 2 + (rel > 0 ? 0 : 1);  // a CTA's first pair may have begun before it, its last go on
+#pragma unroll 1
+    for (int i = threadIdx.x; i < nheads * DP; i += kThreads) {
+      const int head = i / DP, c = i % DP;
+      if (c >= p.d) continue;
+      float top = sm_m[0][head], sum = 0.f, acc = 0.f;
+#pragma unroll
+      for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm_m[x][head]);
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x)
+        sum += sm_l[x][head] * ex2(sm_m[x][head] - top), acc += sm_o[(x * kHeads + head) * DP + c];
+      if (whole) {
+        T* dst = static_cast<T*>(p.out) + ((long long)b * p.Hq + hkv * p.G + head0 + head) * p.d + c;
+        if (SAGE_STORE_OK(p.x_out, dst, 2, &g_decode_error)) *dst = from_f32<T>(sum == 0.f ? 0.f : acc / sum);
       } else {
-#pragma unroll
-        for (int q = 0; q < VB / 16; ++q) {
-          const uint4 v = in && VB * g + 16 * q < p.map.dc ? *reinterpret_cast<const uint4*>(src + 16 * q)
-                                                           : make_uint4(0, 0, 0, 0);
-          vc[r][4 * q] = v.x, vc[r][4 * q + 1] = v.y, vc[r][4 * q + 2] = v.z, vc[r][4 * q + 3] = v.w;
+        float* dst = p.part_o + (long long)(part * kHeads + head) * dc + c;
+        if (SAGE_STORE_OK(p.x_part_o, dst, 4, &g_decode_error)) *dst = acc;
+        if (c == 0) {
+          float* ml = p.part_ml + (part * kHeads + head) * 2;
+          if (SAGE_STORE_OK(p.x_part_ml, ml, 8, &g_decode_error)) ml[0] = top, ml[1] = sum;
         }
       }
     }
-    float kf[2], lv[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const bool in = g + 8 * r < n;
-      kf[r] = in ? p.map.ks[row + g + 8 * r] * p.scale_log2 : 0.f;
-      lv[r] = in ? lg2(p.map.vs[row + g + 8 * r]) : 0.f;
-    }
-
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < KC; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w0 = (&kc[0][c].x)[i], w1 = (&kc[1][c].x)[i];
-        mma16816<T>(s, widen_int8<T, 0>(w0), widen_int8<T, 0>(w1), widen_int8<T, 1>(w0), widen_int8<T, 1>(w1),
-                    qf[4 * c + i][0], qf[4 * c + i][1]);
-      }
-    float w[4];  // s, w: keys g (0, 1) and g + 8 (2, 3) of heads 2t and 2t + 1
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = e >> 1;
-      const bool in = g + 8 * r < n;
-      s[e] = in ? s[e] * kf[r] : -INFINITY;
-      w[e] = in ? s[e] + lv[r] : -INFINITY;
-    }
-    bool move = false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      move |= fmaxf(s[h], s[2 + h]) > ms[h] + kLag || fmaxf(w[h], w[2 + h]) > mw[h] + kLag;
-    if (__any_sync(0xffffffffu, move)) {
-      float f[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float nms = fmaxf(ms[h], max_over_keys(fmaxf(s[h], s[2 + h])));
-        const float nmw = fmaxf(mw[h], max_over_keys(fmaxf(w[h], w[2 + h])));
-        l[h] *= ex2(ms[h] - nms);
-        f[h] = ex2(mw[h] - nmw);
-        ms[h] = nms, mw[h] = nmw;
-      }
-#pragma unroll
-      for (int m = 0; m < VW * 2; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[m][e] *= f[e & 1];
-    }
-    float pw[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      l[e & 1] += ex2(s[e] - ms[e & 1]);
-      pw[e] = ex2(w[e] - mw[e & 1]);
-    }
-    // P^T as B operand: fp16.  For fp16 outputs a second fp16 term carries what the first rounds off
-    // (2^-12 of a weight would be as large as the output's own rounding).
-    uint32_t ph[2], pl[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const __half2 hi = __floats2half2_rn(pw[2 * r], pw[2 * r + 1]);
-      ph[r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
-      if (kSplitP) {
-        const float2 back = __half22float2(hi);
-        const __half2 lo = __floats2half2_rn(pw[2 * r] - back.x, pw[2 * r + 1] - back.y);
-        pl[r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
-      }
-    }
-#pragma unroll
-    for (int wd = 0; wd < VW; ++wd)
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const uint32_t sel = hh ? 0x7362 : 0x5140;
-        const uint32_t x0 = __byte_perm(vc[0][wd], vc[1][wd], sel), x1 = __byte_perm(vc[2][wd], vc[3][wd], sel);
-        const uint32_t a0 = widen_e4m3(x0 & 0xFFFFu), a1 = widen_e4m3(x0 >> 16), a2 = widen_e4m3(x1 & 0xFFFFu),
-                       a3 = widen_e4m3(x1 >> 16);
-        mma16816<__half>(o[2 * wd + hh], a0, a1, a2, a3, ph[0], ph[1]);
-        if (kSplitP) mma16816<__half>(o[2 * wd + hh], a0, a1, a2, a3, pl[0], pl[1]);
-      }
-  }
-
-  // ---- join the warps: O moves to the reference of the scores, then to the largest one
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
-    if (g == 0) sm_m[warp][2 * t + h] = ms[h], sm_l[warp][2 * t + h] = l[h];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int head = 2 * t + h;
-    float top = sm_m[0][head];
-#pragma unroll
-    for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm_m[x][head]);
-    const float f = ex2(mw[h] - top);
-#pragma unroll
-    for (int m = 0; m < VW * 2; ++m) {
-      const int c = VB * g + 2 * m;
-      sm_o[warp][head][c] = o[m][h] * f;
-      sm_o[warp][head][c + 1] = o[m][2 + h] * f;
-    }
-  }
-  __syncthreads();
-  const bool whole = len <= p.chunk;  // this CTA saw the whole sequence
-  for (int i = threadIdx.x; i < nheads * DP; i += kThreads) {
-    const int head = i / DP, c = i % DP;
-    if (c >= p.d) continue;
-    float top = sm_m[0][head], sum = 0.f, acc = 0.f;
-#pragma unroll
-    for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm_m[x][head]);
-#pragma unroll
-    for (int x = 0; x < kWarps; ++x) sum += sm_l[x][head] * ex2(sm_m[x][head] - top), acc += sm_o[x][head][c];
-    const long long hq = (long long)b * p.Hq + hkv * p.G + head0 + head;
-    if (whole) {
-      T* dst = static_cast<T*>(p.out) + hq * p.d + c;
-      if (SAGE_STORE_OK(p.x_out, dst, 2, &g_decode_error)) *dst = from_f32<T>(sum == 0.f ? 0.f : acc / sum);
-    } else {
-      const long long part = hq * p.nsplit + split;
-      float* dst = p.part_o + part * p.d + c;
-      if (SAGE_STORE_OK(p.x_part_o, dst, 4, &g_decode_error)) *dst = acc;
-      if (c == 0) {
-        float* ml = p.part_ml + part * 2;
-        if (SAGE_STORE_OK(p.x_part_ml, ml, 8, &g_decode_error)) ml[0] = top, ml[1] = sum;
-      }
-    }
+    unit += n_seg, pair0 += n_pair;
+    if (unit >= unit_end || sm_dead) return;
+    if (++pair == p.pairs) pair = 0, ++b, len = seq_len_of(p, b, false);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();  // O is read: the rings may be filled again
   }
 }
 
-// Joins the chunks of a sequence: out = sum_i O_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(DecodeParams p) {
-  const long long hq = blockIdx.x;
-  const int len = seq_len_of(p, (int)(hq / p.Hq), false);
-  const int n = (len + p.chunk - 1) / p.chunk;
-  if (n <= 1) return;  // written by the only chunk
-  const float* ml = p.part_ml + hq * p.nsplit * 2;
-  const float* po = p.part_o + hq * p.nsplit * p.d;
-  float top = ml[0];
-  for (int i = 1; i < n; ++i) top = fmaxf(top, ml[2 * i]);
-  float sum = 0.f;
-  for (int i = 0; i < n; ++i) sum += ml[2 * i + 1] * ex2(ml[2 * i] - top);
-  for (int c = threadIdx.x; c < p.d; c += kThreads) {
-    float acc = 0.f;
-    for (int i = 0; i < n; ++i) acc += po[(long long)i * p.d + c] * ex2(ml[2 * i] - top);
-    T* dst = static_cast<T*>(p.out) + hq * p.d + c;
-    if (SAGE_STORE_OK(p.x_out, dst, 2, &g_decode_error)) *dst = from_f32<T>(sum == 0.f ? 0.f : acc / sum);
+// Joins the pairs that cross CTAs: out = sum_i O_i 2^(m_i - M) / sum_i l_i 2^(m_i - M), i over the CTAs that a
+// pair crosses.  CTA c of this kernel looks at the border before CTA c + 1 of the other, and takes the pair there if
+// that is the first border inside it.  Launched as a programmatic dependent: it finds its pair while the
+// other kernel still runs.  Warps share out the tile's heads, then the parts; a warp's loads are in
+// flight eight at a time (one at a time cost 20 us for the 56 parts of a 131072-key sequence).
+constexpr int kJoinWarps = 16, kJoinBatch = 8;
+template <typename T, int V>  // V float4 per lane: d <= 128 V
+__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(DecodeParams p) {
+  __shared__ float4 sm_o[kJoinWarps][32 * V];
+  const Place at = find_place<kJoinWarps * 32>(p, blockIdx.x + 1, false);
+  if (at.b < 0) return;
+  const uint32_t u = (blockIdx.x + 1) * at.share;
+  if (at.pair0 == u || at.pair0 < u - at.share) return;  // no pair crosses here, or it crossed an earlier border
+  const int c0 = blockIdx.x, n = (int)((at.pair0 + units_of(p, at.len) - 1) / at.share) - c0 + 1;
+  const int hkv = at.pair / p.tiles, head0 = (at.pair % p.tiles) * kHeads, nheads = min(kHeads, p.G - head0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dc = p.map.dc;
+  const int ways = kJoinWarps / (nheads > 4 ? 8 : nheads > 2 ? 4 : nheads);  // warps per head
+  const int head = min(warp / ways, nheads - 1), way = warp % ways;
+  // CTA c's part: its last pair's (1) where the pair began, its first one's (0) behind that
+  const auto part = [&](int i) { return (long long)((c0 + i) * 2 + (i == 0 ? 1 : 0)) * kHeads + head; };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float top = -FLT_MAX, sum = 0.f;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[part(i)].x);
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  float4 acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kJoinBatch * ways) {
+    float4 o[kJoinBatch][V];
+    float f[kJoinBatch];
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) {
+      const int i = i0 + k * ways + way;
+      const float2 x = i < n ? ml[part(i)] : make_float2(-INFINITY, 0.f);
+      f[k] = ex2(x.x - top);
+      sum += x.y * f[k];
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        o[k][v] = i < n && 4 * (lane + 32 * v) < dc
+                      ? *reinterpret_cast<const float4*>(p.part_o + part(i) * dc + 4 * (lane + 32 * v))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        acc[v].x += o[k][v].x * f[k], acc[v].y += o[k][v].y * f[k], acc[v].z += o[k][v].z * f[k],
+            acc[v].w += o[k][v].w * f[k];
   }
+  __shared__ float sm_l[kJoinWarps];
+#pragma unroll
+  for (int v = 0; v < V; ++v) sm_o[warp][lane + 32 * v] = acc[v];
+  if (lane == 0) sm_l[warp] = sum;
+  __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < nheads * 128 * V; i += kJoinWarps * 32) {
+    const int h = i / (128 * V), c = i % (128 * V);
+    if (c >= p.d) continue;
+    float num = 0.f, den = 0.f;
+#pragma unroll 1
+    for (int x = h * ways; x < (h + 1) * ways; ++x) num += reinterpret_cast<const float*>(sm_o[x])[c], den += sm_l[x];
+    T* dst = static_cast<T*>(p.out) + ((long long)at.b * p.Hq + hkv * p.G + head0 + h) * p.d + c;
+    if (SAGE_STORE_OK(p.x_out, dst, 2, &g_decode_error)) *dst = from_f32<T>(den == 0.f ? 0.f : num / den);
+  }
+}
+
+template <typename T, int DP>
+cudaError_t launch_decode_dp(const DecodeParams& p, cudaStream_t st) {
+  const auto kernel = decode_kernel<T, DP>;
+  const int smem = Ring<DP>::cta_bytes(p.map.dc);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<p.ctas, kThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t launch_join(const DecodeParams& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(p.ctas - 1), cfg.blockDim = dim3(kJoinWarps * 32), cfg.stream = st;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, V>, p);
 }
 
 template <typename T>
 cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t st) {
-  const dim3 grid(p.nsplit, (p.Hq / p.G) * p.tiles, p.B);
-  if (p.d <= 64)
-    decode_kernel<T, 64><<<grid, kThreads, 0, st>>>(p);
-  else if (p.d <= 128)
-    decode_kernel<T, 128><<<grid, kThreads, 0, st>>>(p);
-  else
-    decode_kernel<T, 256><<<grid, kThreads, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.nsplit == 1) return e;
-  decode_join_kernel<T><<<p.B * p.Hq, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  const cudaError_t e = p.d <= 64    ? launch_decode_dp<T, 64>(p, st)
+                        : p.d <= 128 ? launch_decode_dp<T, 128>(p, st)
+                                     : launch_decode_dp<T, 256>(p, st);
+  if (e != cudaSuccess || !p.part_o) return e;
+  return p.d <= 128 ? launch_join<T, 1>(p, st) : launch_join<T, 2>(p, st);
 }
 
 }  // namespace
+
+int decode_ctas_per_sm(int d) { return d <= 128 ? 3 : 2; }
 
 cudaError_t launch_decode(const DecodeParams& p, int dtype, cudaStream_t st) {
   return dtype == SAGE_FP16 ? launch_decode_t<__half>(p, st) : launch_decode_t<__nv_bfloat16>(p, st);

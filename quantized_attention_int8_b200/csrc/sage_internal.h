@@ -209,6 +209,8 @@ struct GatherParams {
   Extent x_k_out, x_v_out;
 };
 
+constexpr int kDecodeHeads = 8;  // query heads per tile
+
 struct DecodeParams {
   PageMap map;
   HeadView q;  // token stride unused
@@ -216,13 +218,13 @@ struct DecodeParams {
   const int32_t* seq_lens;
   int B, Hq, G, d;
   int max_len;     // longest sequence the launch covers
-  int chunk;       // keys per CTA (a multiple of 64)
-  int nsplit;      // ceil(max_len / chunk)
   int tiles;       // tiles of 8 query heads per kv head
+  uint32_t pairs;  // kv heads x tiles
+  int unit_log2;   // keys per unit of work
+  uint32_t ctas;   // CTAs that share the work evenly
   float scale_log2;
-  float* part_o;   // [B][Hq][nsplit][d]   (nsplit > 1)
-  float* part_ml;  // [B][Hq][nsplit][2]: running max (log2 units) and sum
-  bool vec_q;
+  float* part_o;   // [2 ctas][8][dc]: a CTA's part of the pair that it begins in, and of the one it ends in (or nullptr)
+  float* part_ml;  // [2 ctas][8][2]: running max (log2 units) and sum
   Extent x_out, x_part_o, x_part_ml;
 };
 
@@ -230,6 +232,7 @@ cudaError_t launch_quantize(const QuantParams& p, cudaStream_t st);
 cudaError_t launch_head_rows(const HeadRowsParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_cache_gather(const GatherParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_decode(const DecodeParams& p, int dtype, cudaStream_t st);
+int decode_ctas_per_sm(int d);
 cudaError_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams& p,
                        int dtype, int causal, int pv_mode, cudaStream_t st);
 // Packed batches: per-sequence table from the caller's cumulative lengths (validated on the device;
