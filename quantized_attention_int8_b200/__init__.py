@@ -294,82 +294,100 @@ def sage_attn_noalloc(q, k, v, tensor_layout="HND", is_causal=False, sm_scale=No
 # Serving: head norm and rotation, the paged cache, one-token attention (include/sage.h, "Serving").
 # None of these record gradients.
 # ---------------------------------------------------------------------------------------------
-def _call(device, name, *args):
-    """One C entry point on ``device`` and its current stream."""
-    if device.index == torch.cuda.current_device():
-        st = getattr(capi, name)(*args, torch.cuda.current_stream().cuda_stream)
+# The current stream's handle, without building a torch.cuda.Stream for it (3 us of a decode step's call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(dev, name, *args):
+    """One C entry point on device ``dev`` (an index) and its current stream."""
+    if dev == torch.cuda.current_device():
+        st = getattr(capi, name)(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            st = getattr(capi, name)(*args, torch.cuda.current_stream().cuda_stream)
-    _check(st, name)
+        with torch.cuda.device(dev):
+            st = getattr(capi, name)(*args, _raw_stream(dev))
+    if st != SAGE_OK:
+        _check(st, name)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check_heads(name, t, like=None):
-    """A CUDA tensor of 16-bit heads with contiguous channels, of the dtype and on the device of ``like``."""
-    if not t.is_cuda:
+def _check_heads(name, t, dtype=None, dev=None):
+    """Strides of a CUDA tensor of heads with contiguous channels, of this dtype and on this device (an index)."""
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
     if t.dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {t.dtype} of {name}")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if dtype is not None and (t.dtype != dtype or t.get_device() != dev):
+        raise ValueError(f"{name} must have dtype {dtype} and be on cuda:{dev}, got {t.dtype} on {t.device}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"the channels (last dimension) of {name} must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must have dtype {like.dtype} and be on {like.device}, got {t.dtype} on {t.device}")
+    return st
 
 
-def _check_out(name, t, shape, like):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    _check_heads(name, t, like)
+def _check_out(name, t, like, dev):
+    if t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    return _check_heads(name, t, like.dtype, dev)
 
 
-def _check_ints(name, t, shape, device):
+def _check_ints(name, t, shape, dev):
     """An int32 CUDA tensor of this shape (None: any extent) whose last dimension is contiguous."""
-    if not (t.is_cuda and t.dtype == torch.int32 and t.dim() == len(shape) and t.device == device):
-        raise ValueError(f"{name} must be a {len(shape)}-D int32 tensor on {device}")
-    if any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    s = t.shape
+    if t.dtype is not torch.int32 or t.get_device() != dev or len(s) != len(shape):
+        raise ValueError(f"{name} must be a {len(shape)}-D int32 tensor on cuda:{dev}")
+    for n, m in zip(shape, s):
+        if n is not None and n != m:
+            raise ValueError(f"{name} has shape {tuple(s)}, expected {shape}")
+    if s[-1] > 1 and t.stride()[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
-def _norm_rope(d, device, norm, eps, q_weight, k_weight, cos_sin, interleaved) -> SageNormRope:
-    nr = SageNormRope(norm=int(bool(norm)), eps=float(eps), interleaved=int(bool(interleaved)))
-    if not norm and (q_weight is not None or k_weight is not None):
-        raise ValueError("q_weight and k_weight need norm=True")
-    dtypes = set()
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            if not (w.is_cuda and w.device == device and w.dtype in _DTYPES and w.is_contiguous()
-                    and tuple(w.shape) == (d,)):
-                raise ValueError(f"{name} must be a contiguous fp16, bf16 or fp32 tensor of shape ({d},) on {device}")
-            dtypes.add(w.dtype)
-    if len(dtypes) > 1:
-        raise ValueError("q_weight and k_weight must share one dtype")
-    nr.q_weight, nr.k_weight = _ptr(q_weight), _ptr(k_weight)
-    nr.weight_dtype = _DTYPES[dtypes.pop()] if dtypes else SAGE_FP32
+def _check_floats(name, t, shape, dev):
+    if t.dtype is not torch.float32 or t.get_device() != dev or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on cuda:{dev}")
+
+
+def _norm_rope(d, dev, norm, eps, q_weight, k_weight, cos_sin, interleaved) -> SageNormRope:
+    wdtype = None
+    if q_weight is not None or k_weight is not None:
+        if not norm:
+            raise ValueError("q_weight and k_weight need norm=True")
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is None:
+                continue
+            if w.get_device() != dev or w.dtype not in _DTYPES or tuple(w.shape) != (d,) or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous fp16, bf16 or fp32 tensor of shape ({d},) on cuda:{dev}")
+            if wdtype is not None and w.dtype != wdtype:
+                raise ValueError("q_weight and k_weight must share one dtype")
+            wdtype = w.dtype
+    table, n_pos, rot = None, 0, 0
     if cos_sin is not None:
-        if not (cos_sin.is_cuda and cos_sin.device == device and cos_sin.dtype == torch.float32
-                and cos_sin.dim() == 2 and cos_sin.is_contiguous()):
-            raise ValueError(f"cos_sin must be a contiguous 2-D float32 tensor (positions, rotary_dim) on {device}")
-        nr.cos_sin, nr.n_pos, nr.rot = cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
-    return nr
+        if cos_sin.dtype is not torch.float32 or cos_sin.get_device() != dev or cos_sin.dim() != 2 \
+                or not cos_sin.is_contiguous():
+            raise ValueError(f"cos_sin must be a contiguous 2-D float32 tensor (positions, rotary_dim) on cuda:{dev}")
+        table, (n_pos, rot) = cos_sin.data_ptr(), cos_sin.shape
+    return SageNormRope(1 if norm else 0, eps, _ptr(q_weight), _ptr(k_weight),
+                        SAGE_FP32 if wdtype is None else _DTYPES[wdtype], table, n_pos, rot, 1 if interleaved else 0)
 
 
-def _btn(t, layout):
+def _btn(shape, st, layout):
     """(batches, tokens, heads) and their element strides of a 4-D HND / NHD or a 3-D packed tensor."""
-    if t.dim() == 3:
-        return (1, t.shape[0], t.shape[1]), (0, t.stride(0), t.stride(1))
-    if t.dim() != 4:
+    if len(shape) == 3:
+        return (1, shape[0], shape[1]), (0, st[0], st[1])
+    if len(shape) != 4:
         raise ValueError("q and k must be 4-D, or 3-D (tokens, heads, head_dim)")
     if layout == "HND":
-        return (t.shape[0], t.shape[2], t.shape[1]), (t.stride(0), t.stride(2), t.stride(1))
+        return (shape[0], shape[2], shape[1]), (st[0], st[2], st[1])
     if layout == "NHD":
-        return tuple(t.shape[:3]), tuple(t.stride()[:3])
+        return (shape[0], shape[1], shape[2]), (st[0], st[1], st[2])
     raise ValueError(f"tensor_layout must be 'HND' or 'NHD', got {layout!r}")
+
+
+_Strides8, _Strides12 = ctypes.c_longlong * 8, ctypes.c_longlong * 12
 
 
 def sage_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weight=None, tensor_layout="HND", norm=True,
@@ -382,36 +400,35 @@ def sage_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weigh
     2i and 2i + 1 with interleaved; None: no rotation.  positions int32 (N,) or (B,N), default 0..N-1; one
     outside the table leaves its token unwritten and is reported by sage_check_status.  Weights (d,) in fp16,
     bf16 or fp32.  q_out may be q and k_out may be k."""
-    _check_heads("q", q)
-    (B, N, Hq), qs = _btn(q, tensor_layout)
-    d = q.shape[-1]
-    Hkv, ks = 0, (0, 0, 0)
+    st = _check_heads("q", q)
+    shape, dev = q.shape, q.get_device()
+    (B, N, Hq), qs = _btn(shape, st, tensor_layout)
+    d = shape[-1]
+    Hkv, ks, kos = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
-        _check_heads("k", k, q)
-        (Bk, Nk, Hkv), ks = _btn(k, tensor_layout)
-        if (Bk, Nk, k.shape[-1], k.dim()) != (B, N, d, q.dim()):
-            raise ValueError(f"k of shape {tuple(k.shape)} does not fit q of shape {tuple(q.shape)}")
+        st = _check_heads("k", k, q.dtype, dev)
+        (Bk, Nk, Hkv), ks = _btn(k.shape, st, tensor_layout)
+        if Bk != B or Nk != N or k.shape[-1] != d or len(k.shape) != len(shape):
+            raise ValueError(f"k of shape {tuple(k.shape)} does not fit q of shape {tuple(shape)}")
+        if k_out is None:
+            k_out = k.new_empty(k.shape)
+        kos = _btn(k.shape, _check_out("k_out", k_out, k, dev), tensor_layout)[1]
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
     pos_stride = 0
     if positions is not None:
         if cos_sin is None:
             raise ValueError("positions need cos_sin")
-        _check_ints("positions", positions, (N,) if positions.dim() == 1 else (B, N), q.device)
-        pos_stride = positions.stride(0) if positions.dim() == 2 else 0
+        one = positions.dim() == 1
+        _check_ints("positions", positions, (N,) if one else (B, N), dev)
+        pos_stride = 0 if one else positions.stride(0)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _check_out("q_out", q_out, q.shape, q)
-    kos = (0, 0, 0)
-    if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _check_out("k_out", k_out, k.shape, k)
-        kos = _btn(k_out, tensor_layout)[1]
-    elif k_out is not None:
-        raise ValueError("k_out needs k")
-    nr = _norm_rope(d, q.device, norm, eps, q_weight, k_weight, cos_sin, interleaved)
-    strides = (ctypes.c_longlong * 12)(*qs, *ks, *_btn(q_out, tensor_layout)[1], *kos)
-    _call(q.device, "sage_qk_norm_rope", q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), strides,
-          _ptr(positions), pos_stride, B, N, Hq, Hkv, d, _DTYPES[q.dtype], ctypes.byref(nr))
+        q_out = q.new_empty(shape)
+    qos = _btn(shape, _check_out("q_out", q_out, q, dev), tensor_layout)[1]
+    nr = _norm_rope(d, dev, norm, eps, q_weight, k_weight, cos_sin, interleaved)
+    _call(dev, "sage_qk_norm_rope", q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out),
+          _Strides12(*qs, *ks, *qos, *kos), _ptr(positions), pos_stride, B, N, Hq, Hkv, d, _DTYPES[q.dtype],
+          ctypes.byref(nr))
     return q_out, k_out
 
 
@@ -426,24 +443,20 @@ def sage_kv_cache(num_pages, num_kv_heads, head_dim, page_size=64, device="cuda"
                 vs=torch.zeros(shape, dtype=torch.float32, device=device))
 
 
-def _cache_struct(cache, d, device) -> SageKVCache:
+def _cache_struct(cache, d, dev) -> SageKVCache:
     k8, ks, v8, vs = cache["k8"], cache["ks"], cache["v8"], cache["vs"]
-    for name, t, dtype in (("k8", k8, torch.int8), ("v8", v8, torch.uint8), ("ks", ks, torch.float32),
-                           ("vs", vs, torch.float32)):
-        if not (t.is_cuda and t.device == device and t.dtype == dtype and t.is_contiguous()):
-            raise ValueError(f"cache[{name!r}] must be a contiguous {dtype} tensor on {device}")
-    if k8.dim() != 4 or k8.shape[3] != (d + 15) // 16 * 16:
-        raise ValueError(f"cache['k8'] of shape {tuple(k8.shape)} does not hold heads of {d} channels")
-    if v8.shape != k8.shape or ks.shape != k8.shape[:3] or vs.shape != k8.shape[:3]:
+    if k8.dtype is not torch.int8 or v8.dtype is not torch.uint8 or ks.dtype is not torch.float32 \
+            or vs.dtype is not torch.float32:
+        raise ValueError("the cache holds k8 int8, v8 uint8, ks and vs float32")
+    for t in (k8, ks, v8, vs):
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
+            raise ValueError(f"the cache's arrays must be contiguous CUDA tensors on one device (cuda:{dev})")
+    shape = k8.shape
+    if len(shape) != 4 or shape[3] != (d + 15) // 16 * 16:
+        raise ValueError(f"cache['k8'] of shape {tuple(shape)} does not hold heads of {d} channels")
+    if v8.shape != shape or ks.shape != shape[:3] or vs.shape != shape[:3]:
         raise ValueError("the cache's arrays do not fit one another")
-    return SageKVCache(k8.data_ptr(), ks.data_ptr(), v8.data_ptr(), vs.data_ptr(), k8.shape[0], k8.shape[2],
-                       k8.shape[1], d)
-
-
-def _check_k_mean(k_mean, Hkv, d, device):
-    if k_mean is not None and not (k_mean.is_cuda and k_mean.device == device and k_mean.dtype == torch.float32
-                                   and tuple(k_mean.shape) == (Hkv, d) and k_mean.is_contiguous()):
-        raise ValueError(f"k_mean must be a contiguous float32 tensor of shape ({Hkv}, {d}) on {device}")
+    return SageKVCache(k8.data_ptr(), ks.data_ptr(), v8.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1], d)
 
 
 def sage_cache_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, q=None, cos_sin=None, q_weight=None,
@@ -456,39 +469,40 @@ def sage_cache_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, q=None
     which is returned (q_out; None without q).  k_mean float32 (Hkv,d) is subtracted from the keys before
     they are coded.  Channels contiguous, other strides free.  Bad pages and positions are skipped and reported
     by sage_check_status."""
-    _check_heads("k", k)
-    _check_heads("v", v, k)
-    if k.dim() != 3 or v.shape != k.shape:
+    kst = _check_heads("k", k)
+    dtype, dev, shape = k.dtype, k.get_device(), k.shape
+    vst = _check_heads("v", v, dtype, dev)
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v must be 3-D (tokens, heads, head_dim) and of one shape")
-    T, Hkv, d = k.shape
-    dev = k.device
+    T, Hkv, d = shape
     c = _cache_struct(cache, d, dev)
     if c.Hkv != Hkv:
         raise ValueError(f"the cache has {c.Hkv} heads, k {Hkv}")
     _check_ints("page_table", page_table, (None, None), dev)
-    B = page_table.shape[0]
+    B, max_pages = page_table.shape
     _check_ints("seq_lens", seq_lens, (B,), dev)
     if cu_seqlens is not None:
         _check_ints("cu_seqlens", cu_seqlens, (B + 1,), dev)
     elif T != B:
         raise ValueError(f"{T} tokens for {B} sequences: pass cu_seqlens")
-    _check_k_mean(k_mean, Hkv, d, dev)
-    Hq, qs, qos = 0, (0, 0), (0, 0)
+    if k_mean is not None:
+        _check_floats("k_mean", k_mean, (Hkv, d), dev)
+    Hq, qst, qost = 0, (0, 0), (0, 0)
     if q is not None:
-        _check_heads("q", q, k)
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
-            raise ValueError(f"q of shape {tuple(q.shape)} does not fit k of shape {tuple(k.shape)}")
+        qst = _check_heads("q", q, dtype, dev)
+        if len(q.shape) != 3 or q.shape[0] != T or q.shape[2] != d:
+            raise ValueError(f"q of shape {tuple(q.shape)} does not fit k of shape {tuple(shape)}")
+        Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        _check_out("q_out", q_out, q.shape, q)
-        Hq, qs, qos = q.shape[1], (q.stride(0), q.stride(1)), (q_out.stride(0), q_out.stride(1))
+            q_out = q.new_empty(q.shape)
+        qost = _check_out("q_out", q_out, q, dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     nr = _norm_rope(d, dev, norm, eps, q_weight, k_weight, cos_sin, interleaved)
-    strides = (ctypes.c_longlong * 8)(*qs, k.stride(0), k.stride(1), v.stride(0), v.stride(1), *qos)
-    _call(dev, "sage_cache_append", ctypes.byref(c), _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), strides,
-          page_table.data_ptr(), page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(), _ptr(cu_seqlens),
-          _ptr(k_mean), T, B, Hq, _DTYPES[k.dtype], ctypes.byref(nr))
+    _call(dev, "sage_cache_append", ctypes.byref(c), _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out),
+          _Strides8(qst[0], qst[1], kst[0], kst[1], vst[0], vst[1], qost[0], qost[1]), page_table.data_ptr(),
+          page_table.stride(0), max_pages, seq_lens.data_ptr(), _ptr(cu_seqlens), _ptr(k_mean), T, B, Hq,
+          _DTYPES[dtype], ctypes.byref(nr))
     return q_out
 
 
@@ -499,26 +513,30 @@ def sage_cache_gather(cache, page_table, cu_seqlens, total, head_dim, dtype=torc
     Rows behind the last sequence, and rows of bad pages, are left unwritten."""
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
-    dev = cache["k8"].device
+    k8 = cache["k8"]
+    dev = k8.get_device()
     c = _cache_struct(cache, head_dim, dev)
     _check_ints("page_table", page_table, (None, None), dev)
-    B = page_table.shape[0]
+    B, max_pages = page_table.shape
     _check_ints("cu_seqlens", cu_seqlens, (B + 1,), dev)
     if starts is not None:
         _check_ints("starts", starts, (B,), dev)
-    _check_k_mean(k_mean, c.Hkv, head_dim, dev)
-    shape = (int(total), c.Hkv, head_dim)
-    outs = []
+    if k_mean is not None:
+        _check_floats("k_mean", k_mean, (c.Hkv, head_dim), dev)
+    total = int(total)
+    shape = (total, c.Hkv, head_dim)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        if not (t.is_cuda and t.device == dev and t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
-        outs.append(t)
-    _call(dev, "sage_cache_gather", ctypes.byref(c), page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-          cu_seqlens.data_ptr(), _ptr(starts), _ptr(k_mean), outs[0].data_ptr(), outs[1].data_ptr(), shape[0], B,
+        if t is not None and (t.get_device() != dev or t.dtype != dtype or tuple(t.shape) != shape
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on cuda:{dev}")
+    if k_out is None:
+        k_out = k8.new_empty(shape, dtype=dtype)
+    if v_out is None:
+        v_out = k8.new_empty(shape, dtype=dtype)
+    _call(dev, "sage_cache_gather", ctypes.byref(c), page_table.data_ptr(), page_table.stride(0), max_pages,
+          cu_seqlens.data_ptr(), _ptr(starts), _ptr(k_mean), k_out.data_ptr(), v_out.data_ptr(), total, B,
           _DTYPES[dtype])
-    return outs[0], outs[1]
+    return k_out, v_out
 
 
 def sage_attn_decode(q, cache, page_table, seq_lens, max_seqlen, sm_scale=None, out=None):
@@ -526,21 +544,23 @@ def sage_attn_decode(q, cache, page_table, seq_lens, max_seqlen, sm_scale=None, 
 
     seq_lens int32 (B,): the cached keys each query sees (0: zeros); max_seqlen bounds them (a longer sequence gets
     zeros and is reported by sage_check_status).  q may be strided (channels contiguous)."""
-    _check_heads("q", q)
-    if q.dim() != 3:
+    st = _check_heads("q", q)
+    shape, dev = q.shape, q.get_device()
+    if len(shape) != 3:
         raise ValueError("q must be 3-D (sequences, heads, head_dim)")
-    B, Hq, d = q.shape
-    c = _cache_struct(cache, d, q.device)
-    _check_ints("page_table", page_table, (B, None), q.device)
-    _check_ints("seq_lens", seq_lens, (B,), q.device)
+    B, Hq, d = shape
+    c = _cache_struct(cache, d, dev)
+    _check_ints("page_table", page_table, (B, None), dev)
+    _check_ints("seq_lens", seq_lens, (B,), dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _check_out("out", out, q.shape, q)
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    _call(q.device, "sage_attn_decode", q.data_ptr(), q.stride(0), q.stride(1), ctypes.byref(c), page_table.data_ptr(),
+        out = q.new_empty(shape)
+    else:
+        _check_out("out", out, q, dev)
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+    _call(dev, "sage_attn_decode", q.data_ptr(), st[0], st[1], ctypes.byref(c), page_table.data_ptr(),
           page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(), out.data_ptr(), B, Hq, int(max_seqlen),
-          _DTYPES[q.dtype], float(sm_scale) if sm_scale is not None else 0.0)
+          _DTYPES[q.dtype], 0.0 if sm_scale is None else float(sm_scale))
     return out
 
 

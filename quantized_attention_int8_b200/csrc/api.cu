@@ -691,29 +691,45 @@ bool vec_view(const HeadView& v, long long B, long long N, long long H) {
          (H == 1 || v.head % 8 == 0);
 }
 
+// Checks the views' extents, and takes from their alignment whether rows go in vectors.
+sage_status take_views(HeadRowsParams* p, int batches) {
+  for (HeadRows& k : p->kind)
+    for (const HeadView* v : {&k.in, &k.out}) {
+      if (!k.H || !v->ptr) continue;
+      if (!view_fits(*v, batches, p->N, k.H)) return SAGE_ERR_INVALID_ARG;
+      p->vec = p->vec && vec_view(*v, batches, p->N, k.H);
+      if (v == &k.out) k.x_out = extent_of(v->ptr, view_bytes(*v, batches, p->N, k.H, p->d));
+    }
+  return SAGE_OK;
+}
+
 void set_norm_rope(HeadRowsParams* p, const sage_norm_rope& nr) {
   p->norm = nr.norm ? 1 : 0, p->eps = nr.eps, p->inv_d = 1.0f / (float)p->d;
-  p->q_weight = nr.q_weight, p->k_weight = nr.k_weight, p->weight_dtype = nr.weight_dtype;
+  p->kind[0].weight = nr.q_weight, p->kind[1].weight = nr.k_weight, p->weight_dtype = nr.weight_dtype;
   p->vec_weight = p->d % 8 == 0 && aligned16(nr.q_weight) && aligned16(nr.k_weight);
   p->cos_sin = nr.cos_sin, p->n_pos = nr.n_pos, p->rot = nr.cos_sin ? nr.rot : 0, p->interleaved = nr.interleaved ? 1 : 0;
-  // a lane's eight channels lie in one half of the rotated ones, and its table entries in 16-byte vectors
-  if (nr.cos_sin && !nr.interleaved) p->vec = p->vec && nr.rot % 16 == 0 && aligned16(nr.cos_sin);
+  // a lane's pairs, four in a row, are all rotated or none is; its cosines and its sines are 16-byte vectors
+  if (nr.cos_sin) p->vec = p->vec && nr.rot % 8 == 0 && aligned16(nr.cos_sin);
 }
 
 // Launch shape: groups take four heads of a token where that still gives every SM its full 2048
 // threads, else one.
-sage_status shape_rows(HeadRowsParams* p, int batches, int kinds_kv) {
+sage_status shape_rows(HeadRowsParams* p, int batches) {
   const int lanes = p->d <= 64 ? 8 : p->d <= 128 ? 16 : 32;
   const long long tokens = (long long)batches * p->N;
   if (tokens > kMaxItems) return SAGE_ERR_INVALID_ARG;
-  const auto chunks = [&](int hc) {
-    p->q_chunks = (p->Hq + hc - 1) / hc, p->k_chunks = (p->Hkv + hc - 1) / hc;
-    p->chunks = p->q_chunks + kinds_kv * p->k_chunks;
-    return tokens * p->chunks;
+  const auto items = [&](int hc) {
+    long long n = 0;
+    for (const HeadRows& k : p->kind) n += tokens * ((k.H + hc - 1) / hc);
+    return n;
   };
-  p->heads_per_group = p->vec && chunks(4) * lanes >= 148LL * 2048 ? 4 : 1;
-  p->items = chunks(p->heads_per_group);
-  return p->items > kMaxItems ? SAGE_ERR_INVALID_ARG : SAGE_OK;
+  p->heads_per_group = p->vec && items(4) * lanes >= 148LL * 2048 ? 4 : 1;
+  if (items(p->heads_per_group) > kMaxItems) return SAGE_ERR_INVALID_ARG;
+  for (HeadRows& k : p->kind) {
+    k.chunks = (k.H + p->heads_per_group - 1) / p->heads_per_group;
+    k.items = (unsigned)(tokens * k.chunks);
+  }
+  return SAGE_OK;
 }
 
 }  // namespace
@@ -735,22 +751,16 @@ sage_status sage_qk_norm_rope(const void* q, const void* k, void* q_out, void* k
   if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)q_out | (uintptr_t)k_out) & 1) return SAGE_ERR_INVALID_ARG;
   HeadRowsParams p;
   memset(&p, 0, sizeof(p));
-  p.B = B, p.N = N, p.Hq = Hq, p.Hkv = k ? Hkv : 0, p.d = d;
-  p.q = HeadView{q, strides[0], strides[1], strides[2]};
-  p.k = HeadView{k, strides[3], strides[4], strides[5]};
-  p.q_out = HeadView{q_out, strides[6], strides[7], strides[8]};
-  p.k_out = HeadView{k_out, strides[9], strides[10], strides[11]};
-  if (!view_fits(p.q, B, N, Hq) || !view_fits(p.q_out, B, N, Hq) ||
-      (k && (!view_fits(p.k, B, N, Hkv) || !view_fits(p.k_out, B, N, Hkv))))
-    return SAGE_ERR_INVALID_ARG;
+  p.B = B, p.N = N, p.d = d, p.vec = d % 8 == 0;
+  p.kind[0].in = HeadView{q, strides[0], strides[1], strides[2]}, p.kind[0].H = Hq;
+  p.kind[1].in = HeadView{k, strides[3], strides[4], strides[5]}, p.kind[1].H = k ? Hkv : 0;
+  p.kind[0].out = HeadView{q_out, strides[6], strides[7], strides[8]};
+  p.kind[1].out = HeadView{k_out, strides[9], strides[10], strides[11]};
+  if ((s = take_views(&p, B)) != SAGE_OK) return s;
   p.positions = positions, p.pos_batch = pos_batch_stride;
-  p.vec = d % 8 == 0 && vec_view(p.q, B, N, Hq) && vec_view(p.q_out, B, N, Hq) &&
-          (!k || (vec_view(p.k, B, N, Hkv) && vec_view(p.k_out, B, N, Hkv)));
   set_norm_rope(&p, *nr);
-  p.token_fast = p.q.token < p.q.head;
-  p.x_q_out = extent_of(q_out, view_bytes(p.q_out, B, N, Hq, d));
-  if (k) p.x_k_out = extent_of(k_out, view_bytes(p.k_out, B, N, Hkv, d));
-  if ((s = shape_rows(&p, B, 1)) != SAGE_OK) return s;
+  p.token_fast = p.kind[0].in.token < p.kind[0].in.head;
+  if ((s = shape_rows(&p, B)) != SAGE_OK) return s;
   if ((s = check_device()) != SAGE_OK) return s;
   return from_cuda(launch_head_rows(p, dtype, static_cast<cudaStream_t>(stream)));
 }
@@ -773,24 +783,19 @@ sage_status sage_cache_append(const sage_kv_cache* cache, const void* q, const v
   if (!k || !v || !seq_lens || (q && !q_out)) return SAGE_ERR_INVALID_ARG;
   if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out) & 1) return SAGE_ERR_INVALID_ARG;
   const int d = cache->d, Hkv = cache->Hkv;
-  p.B = B, p.N = T, p.Hq = q ? Hq : 0, p.Hkv = Hkv, p.d = d;
-  p.q = HeadView{q, 0, strides[0], strides[1]};
-  p.k = HeadView{k, 0, strides[2], strides[3]};
-  p.v = HeadView{v, 0, strides[4], strides[5]};
-  p.q_out = HeadView{q_out, 0, strides[6], strides[7]};
-  if (!view_fits(p.k, 1, T, Hkv) || !view_fits(p.v, 1, T, Hkv) ||
-      (q && (!view_fits(p.q, 1, T, Hq) || !view_fits(p.q_out, 1, T, Hq))))
-    return SAGE_ERR_INVALID_ARG;
+  p.B = B, p.N = T, p.d = d, p.vec = d % 8 == 0;
+  p.kind[0].in = HeadView{q, 0, strides[0], strides[1]}, p.kind[0].H = q ? Hq : 0;
+  p.kind[1].in = HeadView{k, 0, strides[2], strides[3]}, p.kind[1].H = Hkv;
+  p.kind[2].in = HeadView{v, 0, strides[4], strides[5]}, p.kind[2].H = Hkv;
+  p.kind[0].out = HeadView{q_out, 0, strides[6], strides[7]};
+  if ((s = take_views(&p, 1)) != SAGE_OK) return s;
   p.append = 1, p.cu = cu_seqlens, p.seq_lens = seq_lens, p.k_mean = k_mean;
-  p.vec = d % 8 == 0 && vec_view(p.k, 1, T, Hkv) && vec_view(p.v, 1, T, Hkv) &&
-          (!q || (vec_view(p.q, 1, T, Hq) && vec_view(p.q_out, 1, T, Hq)));
   p.vec_mean = d % 8 == 0 && aligned16(k_mean);
   if (nr) set_norm_rope(&p, *nr);
-  if (q) p.x_q_out = extent_of(q_out, view_bytes(p.q_out, 1, T, Hq, d));
   const size_t rows = cache_rows(p.map);
   p.x_k8 = extent_of(cache->k8, rows * p.map.dc), p.x_v8 = extent_of(cache->v8, rows * p.map.dc);
   p.x_ks = extent_of(cache->ks, rows * 4), p.x_vs = extent_of(cache->vs, rows * 4);
-  if ((s = shape_rows(&p, 1, 2)) != SAGE_OK) return s;
+  if ((s = shape_rows(&p, 1)) != SAGE_OK) return s;
   if ((s = check_device()) != SAGE_OK) return s;
   return from_cuda(launch_head_rows(p, dtype, static_cast<cudaStream_t>(stream)));
 }

@@ -26,6 +26,7 @@
 //
 // V's scale is folded into the weights: w_j = s_j + log2(vs_j) has a running reference of its own, so
 // the fp16 weights 2^(w_j - ref) keep their precision whatever the scales' spread; the sum uses s_j.
+#include <atomic>
 #include <cfloat>
 #include <type_traits>
 
@@ -635,10 +636,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(DecodePara
 template <typename T, int DP>
 cudaError_t launch_decode_dp(const DecodeParams& p, cudaStream_t st) {
   const auto kernel = decode_kernel<T, DP>;
-  const int smem = Ring<DP>::cta_bytes(p.map.dc);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // once per device: setting it twice does no harm
+  static std::atomic<bool> ready[128];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  kernel<<<p.ctas, kThreads, smem, st>>>(p);
+  if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<DP>::cta_bytes(DP));
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_release);
+  }
+  kernel<<<p.ctas, kThreads, Ring<DP>::cta_bytes(p.map.dc), st>>>(p);
   return cudaGetLastError();
 }
 

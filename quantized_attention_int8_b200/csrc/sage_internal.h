@@ -171,15 +171,26 @@ struct HeadView {
   long long batch, token, head;
 };
 
+// The heads of one kind (Q, K or V) of a pass over head rows.
+struct HeadRows {
+  HeadView in, out;  // out.ptr nullptr: to the cache
+  const void* weight;  // [d] or nullptr
+  int H;
+  Extent x_out;
+  // launch shape: items of `heads_per_group` heads of one token, shared out over `ctas` CTAs in rounds of their
+  // groups (one round more for the first `rounds_more`).  An item's digits are (fastest first) token and chunk of
+  // heads, or chunk and token, then batch.
+  unsigned chunks, items, ctas, rounds, rounds_more, step[3];
+  long long in_step, in_carry[2], out_step, out_carry[2];  // what the addresses move by, and at the digits' carries
+};
+
 struct HeadRowsParams {
-  HeadView q, k, v, q_out, k_out;
-  int B, N, Hq, Hkv, d;  // append: N packed tokens of B sequences
+  HeadRows kind[3];  // Q, K, V
+  int B, N, d;       // append: N packed tokens of B sequences
   const int32_t* positions;  // [B][N], rows pos_batch apart; nullptr: token n is at position n
   long long pos_batch;
   int norm, weight_dtype;
   float eps, inv_d;
-  const void* q_weight;
-  const void* k_weight;
   const float* cos_sin;  // [n_pos][rot]: rot / 2 cosines, then as many sines; nullptr: no rotation
   int n_pos, rot, interleaved;
   // cache write
@@ -188,12 +199,11 @@ struct HeadRowsParams {
   const int32_t* seq_lens;  // [B] lengths with the new tokens
   const float* k_mean;      // [Hkv][d] or nullptr
   PageMap map;
-  // launch shape
-  int heads_per_group, q_chunks, k_chunks, chunks;
+  int heads_per_group;
+  int apart;       // each kind has CTAs of its own (else every CTA takes a share of each)
   int token_fast;  // consecutive groups take consecutive tokens (else consecutive heads of one token)
-  long long items;
   bool vec, vec_weight, vec_mean;
-  Extent x_q_out, x_k_out, x_k8, x_ks, x_v8, x_vs;
+  Extent x_k8, x_ks, x_v8, x_vs;
 };
 
 struct GatherParams {
