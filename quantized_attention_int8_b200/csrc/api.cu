@@ -628,7 +628,7 @@ namespace {
 
 // Strides, and every view's extent along each dimension, stay below these, so that no offset passes 2^63.
 constexpr long long kMaxStride = 1LL << 40, kMaxExtent = 1LL << 48;
-constexpr long long kMaxItems = (1LL << 31) - 1;  // row groups of one launch (32-bit item numbers)
+constexpr long long kMaxItems = 1LL << 31;  // row groups of one launch (32-bit numbers)
 
 sage_status check_strides(const long long* s, int n) {
   if (!s) return SAGE_ERR_INVALID_ARG;
@@ -712,23 +712,26 @@ void set_norm_rope(HeadRowsParams* p, const sage_norm_rope& nr) {
   if (nr.cos_sin) p->vec = p->vec && nr.rot % 8 == 0 && aligned16(nr.cos_sin);
 }
 
-// Launch shape: groups take four heads of a token where that still gives every SM its full 2048
-// threads, else one.
+// Heads of a token that a group of lanes takes at a time: four (fewer instructions per row, more loads in
+// flight per thread) where `items` such groups still give every SM 2048 threads, else one (more
+// threads at work on a short call: a decode step of 64 tokens).
+int rows_per_group(bool vec, int d, long long items) {
+  const int lanes = d <= 64 ? 8 : d <= 128 ? 16 : 32;
+  return vec && items * lanes >= 148LL * 2048 ? 4 : 1;
+}
+
 sage_status shape_rows(HeadRowsParams* p, int batches) {
-  const int lanes = p->d <= 64 ? 8 : p->d <= 128 ? 16 : 32;
   const long long tokens = (long long)batches * p->N;
   if (tokens > kMaxItems) return SAGE_ERR_INVALID_ARG;
   const auto items = [&](int hc) {
     long long n = 0;
-    for (const HeadRows& k : p->kind) n += tokens * ((k.H + hc - 1) / hc);
+    for (const HeadRows& k : p->kind) n += (tokens + 15) * ((k.H + hc - 1) / hc);  // (whole rounds)
     return n;
   };
-  p->heads_per_group = p->vec && items(4) * lanes >= 148LL * 2048 ? 4 : 1;
+  p->heads_per_group = rows_per_group(p->vec, p->d, items(4));
   if (items(p->heads_per_group) > kMaxItems) return SAGE_ERR_INVALID_ARG;
-  for (HeadRows& k : p->kind) {
-    k.chunks = (k.H + p->heads_per_group - 1) / p->heads_per_group;
-    k.items = (unsigned)(tokens * k.chunks);
-  }
+  p->tokens = (unsigned)tokens;
+  for (HeadRows& k : p->kind) k.chunks = (k.H + p->heads_per_group - 1) / p->heads_per_group;
   return SAGE_OK;
 }
 
@@ -759,7 +762,6 @@ sage_status sage_qk_norm_rope(const void* q, const void* k, void* q_out, void* k
   if ((s = take_views(&p, B)) != SAGE_OK) return s;
   p.positions = positions, p.pos_batch = pos_batch_stride;
   set_norm_rope(&p, *nr);
-  p.token_fast = p.kind[0].in.token < p.kind[0].in.head;
   if ((s = shape_rows(&p, B)) != SAGE_OK) return s;
   if ((s = check_device()) != SAGE_OK) return s;
   return from_cuda(launch_head_rows(p, dtype, static_cast<cudaStream_t>(stream)));
@@ -821,9 +823,10 @@ sage_status sage_cache_gather(const sage_kv_cache* cache, const int32_t* page_ta
       return SAGE_ERR_INVALID_ARG;
   p.cu = cu_seqlens, p.starts = starts, p.k_mean = k_mean, p.k_out = k_out, p.v_out = v_out;
   p.B = B, p.T = T, p.d = cache->d;
-  p.items = (long long)T * cache->Hkv;
-  if (p.items > kMaxItems) return SAGE_ERR_INVALID_ARG;
+  const int hkv = cache->Hkv;
+  if (((long long)T + 15) * hkv > kMaxItems) return SAGE_ERR_INVALID_ARG;
   p.vec = cache->d % 8 == 0 && aligned16(k_out) && aligned16(v_out);
+  p.heads_per_group = rows_per_group(p.vec, p.d, (long long)T * ((hkv + 3) / 4));
   p.vec_mean = cache->d % 8 == 0 && aligned16(k_mean);
   p.x_k_out = extent_of(k_out, bytes), p.x_v_out = extent_of(v_out, bytes);
   if ((s = check_device()) != SAGE_OK) return s;

@@ -278,24 +278,25 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
     else
       a = p.rot + 8 * (lane - (half >> 2)), b = a + 4;
   }
-  // This CTA's run of rounds of its groups; a group's items are kGroups apart.
-  const unsigned first = (cta * k.rounds + min(cta, k.rounds_more)) * kGroups;
-  const unsigned end = min(first + (k.rounds + (cta < k.rounds_more ? 1 : 0)) * kGroups, k.items);
-  if (first >= end) return;
-  const unsigned r0 = p.token_fast ? p.N : k.chunks, r1 = p.token_fast ? k.chunks : p.N;
-  unsigned item = first + group;
-  unsigned d0 = item % r0, d1 = item / r0, batch = d1 / r1;
-  d1 -= batch * r1;
+  // This CTA's run of rounds.  A round: one chunk of heads of kGroups tokens, a group each; the chunks run
+  // faster than the tokens, so that a group looks its token up once for all of them, and the groups'
+  // rows are neighbours in every layout (and in the cache).
+  const unsigned rounds = k.rounds + (cta < k.rounds_more ? 1 : 0);
+  if (rounds == 0) return;
+  const unsigned round0 = cta * k.rounds + min(cta, k.rounds_more);
+  unsigned chunk = round0 % k.chunks, t_flat = round0 / k.chunks * kGroups + group, n, batch;
   const unsigned short* src;
   unsigned short* dst;
-  {
-    const unsigned n = p.token_fast ? d0 : d1, h = (p.token_fast ? d1 : d0) * HC;
-    src = static_cast<const unsigned short*>(k.in.ptr) + batch * k.in.batch + n * k.in.token + h * k.in.head;
-    dst = static_cast<unsigned short*>(const_cast<void*>(k.out.ptr)) + batch * k.out.batch + n * k.out.token + h * k.out.head;
-  }
+  const auto place_at_token = [&] {
+    batch = t_flat / (unsigned)p.N, n = t_flat - batch * p.N;
+    src = static_cast<const unsigned short*>(k.in.ptr) + batch * k.in.batch + n * k.in.token + chunk * k.in_chunk;
+    dst = static_cast<unsigned short*>(const_cast<void*>(k.out.ptr)) + batch * k.out.batch + n * k.out.token +
+          chunk * k.out_chunk;
+  };
+  place_at_token();
   uint4 raw[HC];
   const auto load_item = [&] {
-    const int nh = item < end ? k.H - (int)(p.token_fast ? d1 : d0) * HC : 0;
+    const int nh = t_flat < p.tokens ? k.H - (int)chunk * HC : 0;
 #pragma unroll
     for (int i = 0; i < HC; ++i) raw[i] = i < nh ? load8<MODE>(src + i * k.in.head, a, b, p.d) : make_uint4(0, 0, 0, 0);
   };
@@ -311,66 +312,78 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
     for (int e = 0; e < 4; ++e) w[e] = make_float2(f[2 * e], f[2 * e + 1]);
   }
   const bool turn = MODE == kHalves ? a < half : a < p.rot;  // this lane's channels turn (rot 0: none does)
+  // of the token last looked up
+  unsigned token = ~0u;
+  bool token_ok = false;
+  float4 cs, sn;
+  const float* angles = p.cos_sin;  // (groups without an item read row 0 as well)
+  uint8_t* codes = nullptr;
+  float* scales = nullptr;
+  const long long head_rows = 1LL << p.map.page_log2, head_codes = head_rows * p.map.dc;
 
   // Every lane of a warp makes the same number of rounds: the shuffles need them all.
 #pragma unroll 1
-  for (unsigned round = first; round < end; round += kGroups) {
+  for (unsigned round = 0; round < rounds; ++round) {
     uint4 cur[HC];
 #pragma unroll
     for (int i = 0; i < HC; ++i) cur[i] = raw[i];
-    const unsigned n = p.token_fast ? d0 : d1, cbatch = batch;
-    const int h0 = (int)(p.token_fast ? d1 : d0) * HC;
-    bool live = item < end;
+    const unsigned cn = n, cbatch = batch, ct = t_flat;
+    const int h0 = (int)chunk * HC;
+    const bool there = t_flat < p.tokens;
     unsigned short* const out = dst;
-    // ---- the next item's heads
-    item += kGroups;
-    src += k.in_step;
-    if (!kCoded) dst += k.out_step;
-    d0 += k.step[0], d1 += k.step[1], batch += k.step[2];
-    if (d0 >= r0) {
-      d0 -= r0, ++d1, src += k.in_carry[0];
-      if (!kCoded) dst += k.out_carry[0];
-    }
-    if (d1 >= r1) {
-      d1 -= r1, ++batch, src += k.in_carry[1];
-      if (!kCoded) dst += k.out_carry[1];
+    // ---- the next round's heads
+    if (++chunk == k.chunks) {
+      chunk = 0, t_flat += kGroups;
+      if (n + kGroups < (unsigned)p.N) {
+        n += kGroups, src += k.in_tokens;
+        if (!kCoded) dst += k.out_tokens;
+      } else {
+        place_at_token();
+      }
+    } else {
+      src += k.in_chunk;
+      if (!kCoded) dst += k.out_chunk;
     }
     load_item();
 
-    // ---- this token's position, and its place in the cache
-    int pos = 0, page = -1;
-    if (APPEND) {
-      const int t = (int)n;
-      if (p.cu) {
-        if (live && (t < seq_first || t >= seq_end)) {
-          int count = 0;
-          live = find_sequence(p.cu, p.B, t, p.N, &seq, &seq_first, &count);
-          seq_end = live ? seq_first + count : -1;
-          if (live) seq_base = p.seq_lens[seq] - seq_end;
+    // ---- this token's position, its cosines, and its place in the cache
+    if (there && ct != token) {
+      token = ct, token_ok = true;
+      int pos = 0, page = -1;
+      if (APPEND) {
+        const int t = (int)cn;
+        if (p.cu) {
+          if (t < seq_first || t >= seq_end) {
+            int count = 0;
+            token_ok = find_sequence(p.cu, p.B, t, p.N, &seq, &seq_first, &count);
+            seq_end = token_ok ? seq_first + count : -1;
+            if (token_ok) seq_base = p.seq_lens[seq] - seq_end;
+          }
+        } else {
+          seq = t, seq_base = p.seq_lens[t] - 1 - t;
+          if (seq_base == -1 - t) token_ok = false;  // a padded slot of a decode batch
         }
-      } else if (live) {
-        seq = t, seq_base = p.seq_lens[t] - 1 - t;
-        if (seq_base == -1 - t) live = false;  // a padded slot of a decode batch
+        pos = seq_base + t;
+        if (token_ok) page = page_of(p.map, seq, pos), token_ok = page >= 0;
+      } else if (p.cos_sin) {
+        pos = p.positions ? p.positions[cbatch * p.pos_batch + cn] : (int)cn;
       }
-      pos = seq_base + t;
-      if (live) {
-        page = page_of(p.map, seq, pos);
-        live = page >= 0;
+      if (p.cos_sin && token_ok && (unsigned)pos >= (unsigned)p.n_pos) {
+        atomicOr(&g_cache_error, kBadArg);
+        token_ok = false;
       }
-    } else if (p.cos_sin) {
-      pos = p.positions && live ? p.positions[cbatch * p.pos_batch + n] : (int)n;
+      angles = p.cos_sin + (token_ok ? (long long)pos * p.rot : 0);
+      if (KIND != kV && MODE != kScalar && turn) {
+        cs = __ldg(reinterpret_cast<const float4*>(angles + (MODE == kHalves ? a : a >> 1)));
+        sn = __ldg(reinterpret_cast<const float4*>(angles + half + (MODE == kHalves ? a : a >> 1)));
+      }
+      if (kCoded && token_ok) {
+        const long long row = p.map.row(page, 0, pos);
+        codes = (KIND == kK ? reinterpret_cast<uint8_t*>(p.map.k8) : p.map.v8) + row * p.map.dc;
+        scales = (KIND == kK ? p.map.ks : p.map.vs) + row;
+      }
     }
-    if (p.cos_sin && live && (unsigned)pos >= (unsigned)p.n_pos) {
-      atomicOr(&g_cache_error, kBadArg);
-      live = false;
-    }
-    const float* angles = p.cos_sin + (live ? (long long)pos * p.rot : 0);
-    float4 cs, sn;
-    if (KIND != kV && MODE != kScalar && turn) {
-      cs = __ldg(reinterpret_cast<const float4*>(angles + (MODE == kHalves ? a : a >> 1)));
-      sn = __ldg(reinterpret_cast<const float4*>(angles + half + (MODE == kHalves ? a : a >> 1)));
-    }
-    const long long row0 = kCoded && live ? p.map.row(page, h0, pos) : 0;
+    const bool live = there && token_ok;
 
     const bool norm = KIND != kV && p.norm;
     float r = 1.f;  // reduce_rows' layout
@@ -386,10 +399,16 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
       }
       r = rsqrtf(reduce_rows<LPR, HC, false>(ss) * p.inv_d + p.eps);
     }
-    float2 coded[kCoded ? HC : 1][4];
+    float2 coded[KIND == kK && kCoded ? HC : 1][4];
     float amax[HC];
 #pragma unroll
     for (int i = 0; i < HC; ++i) {
+      if (KIND == kV) {  // on the bit patterns: a NaN or an infinity is the largest
+        const uint32_t m = __vmaxu2(__vmaxu2(cur[i].x & 0x7FFF7FFFu, cur[i].y & 0x7FFF7FFFu),
+                                    __vmaxu2(cur[i].z & 0x7FFF7FFFu, cur[i].w & 0x7FFF7FFFu));
+        amax[i] = bits_to_f32<T>(max(m & 0xFFFFu, m >> 16));
+        continue;
+      }
       float2 x[4];
       unpack8<T>(cur[i], x);
       if (norm) {
@@ -438,7 +457,7 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
         continue;
       }
       if (KIND == kK && p.k_mean && (HC == 1 || h0 + i < k.H)) {
-        const float* mean = p.k_mean + (live ? (h0 + i) * p.d : 0);
+        const float* mean = p.k_mean + (there ? (h0 + i) * p.d : 0);
         float m[8];
         load4_param(mean, SAGE_FP32, p.vec_mean, a, p.d, m);
         load4_param(mean, SAGE_FP32, p.vec_mean, b, p.d, m + 4);
@@ -448,23 +467,25 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
       }
       float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = max_nan(max_nan(top, fabsf(x[e].x)), fabsf(x[e].y)), coded[kCoded ? i : 0][e] = x[e];
+      for (int e = 0; e < 4; ++e) top = max_nan(max_nan(top, fabsf(x[e].x)), fabsf(x[e].y)), coded[KIND == kK && kCoded ? i : 0][e] = x[e];
       amax[i] = top;
     }
     if (!kCoded) continue;
     float scale, inv;  // reduce_rows' layout
     code_scale(reduce_rows<LPR, HC, true>(amax), KIND == kK ? 127.f : 448.f, &scale, &inv);
+    const bool odd = __any_sync(0xffffffffu, inv == 0.f);  // a row of zeros, or with a NaN or an infinity: codes 0
 #pragma unroll
     for (int i = 0; i < HC; ++i) {
       const float iv = of_row<LPR, HC>(inv, i);
       const float2 inv2 = make_float2(iv, iv);
-      const float2(&x)[4] = coded[kCoded ? i : 0];
+      float2 vx[4];
+      if (KIND == kV) unpack8<T>(cur[i], vx);
+      const float2(&x)[4] = KIND == kV ? vx : coded[KIND == kK && kCoded ? i : 0];
       uint32_t w0 = KIND == kK ? code4_int8(x[0], x[1], inv2) : code4_e4m3(x[0], x[1], inv2);
       uint32_t w1 = KIND == kK ? code4_int8(x[2], x[3], inv2) : code4_e4m3(x[2], x[3], inv2);
-      if (iv == 0.f) w0 = w1 = 0;  // also where a NaN or an infinity times 0 went into the codes
+      if (odd && iv == 0.f) w0 = w1 = 0;
       if (live && (HC == 1 || h0 + i < k.H)) {
-        const long long row = row0 + ((long long)i << p.map.page_log2);
-        uint8_t* code = (KIND == kK ? reinterpret_cast<uint8_t*>(p.map.k8) : p.map.v8) + row * p.map.dc;
+        uint8_t* const code = codes + (h0 + i) * head_codes;
         const Extent& xc = KIND == kK ? p.x_k8 : p.x_v8;
         if (MODE == kHalves) {
           if (a < p.map.dc && SAGE_STORE_OK(xc, code + a, 4, &g_cache_error)) *reinterpret_cast<uint32_t*>(code + a) = w0;
@@ -475,7 +496,7 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
       }
     }
     const int my_row = HC == 1 ? 0 : 2 * (lane & 1) + (lane >> 1 & 1);
-    float* sdst = (KIND == kK ? p.map.ks : p.map.vs) + row0 + ((long long)my_row << p.map.page_log2);
+    float* sdst = scales + (h0 + my_row) * head_rows;
     if (lane < HC && live && h0 + my_row < k.H && SAGE_STORE_OK(KIND == kK ? p.x_ks : p.x_vs, sdst, 4, &g_cache_error))
       *sdst = scale;
   }
@@ -484,7 +505,7 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
 // Large calls: every CTA takes its share of each kind, one after the other, so that all end together
 // whatever a kind's rows cost.  Small ones (`apart`): the kinds have CTAs of their own, which work at the same time.
 template <typename T, int LPR, int HC, int MODE, bool APPEND>
-__global__ void __launch_bounds__(kThreads, HC > 1 ? 5 : 8) head_rows_kernel(const __grid_constant__ HeadRowsParams p) {
+__global__ void __launch_bounds__(kThreads, HC > 1 ? (APPEND ? 5 : 6) : 8) head_rows_kernel(const __grid_constant__ HeadRowsParams p) {
   __shared__ float partner_buf[MODE == kScalar ? kThreads * 8 : 1];
   const unsigned cta = blockIdx.x, q = p.apart ? p.kind[kQ].ctas : 0, k = p.apart ? q + p.kind[kK].ctas : 0;
   if (!p.apart || cta < q) head_rows<T, LPR, HC, MODE, APPEND, kQ>(p, p.kind[kQ], cta, partner_buf);
@@ -494,59 +515,100 @@ __global__ void __launch_bounds__(kThreads, HC > 1 ? 5 : 8) head_rows_kernel(con
 }
 
 // ------------------------------------------------------------------------------------------ read back
-// One group of LPR lanes per (token, kv head): 16 K and 16 V codes to a lane, read as 16-byte
-// vectors, written as 16-bit values.
-template <typename T, int LPR, bool VEC>
-__global__ void __launch_bounds__(kThreads) gather_kernel(GatherParams p) {
-  constexpr int kGroups = kThreads / LPR;
-  const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR, c0 = lane * 16;
-  const unsigned item = blockIdx.x * (unsigned)kGroups + group;
-  if (item >= (unsigned)p.items || c0 >= p.map.dc) return;
-  const unsigned t = item / (unsigned)p.map.Hkv;
-  const int h = (int)(item % (unsigned)p.map.Hkv);
-  int seq, first, count;
-  if (!find_sequence(p.cu, p.B, (int)t, p.T, &seq, &first, &count)) return;
-  const int pos = (int)t - first + (p.starts ? p.starts[seq] : 0);
-  const int page = page_of(p.map, seq, pos);
-  if (page < 0) return;
-  const long long row = p.map.row(page, h, pos);
-  const uint4 kc = *reinterpret_cast<const uint4*>(p.map.k8 + row * p.map.dc + c0);
-  const uint4 vc = *reinterpret_cast<const uint4*>(p.map.v8 + row * p.map.dc + c0);
-  const float ks = p.map.ks[row], vs = p.map.vs[row];
-  unsigned short* ko = static_cast<unsigned short*>(p.k_out) + (long long)item * p.d;
-  unsigned short* vo = static_cast<unsigned short*>(p.v_out) + (long long)item * p.d;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int c = c0 + 8 * q;
-    float2 x[4];
-    float m[8];
-    if (p.k_mean) {
-      load4_param(p.k_mean + (size_t)h * p.d, SAGE_FP32, p.vec_mean, c, p.d, m);
-      load4_param(p.k_mean + (size_t)h * p.d, SAGE_FP32, p.vec_mean, c + 4, p.d, m + 4);
+// The same rounds: a group of LPR lanes takes HC heads of one token, eight K and eight V codes of each to a
+// lane (8-byte loads, 16-byte stores: both whole sectors), the next round's codes on their way meanwhile.
+// Lanes 0 .. HC-1 hold the K scales of the HC heads, the next HC lanes the V scales.
+template <typename T, int LPR, int HC, bool VEC>
+__global__ void __launch_bounds__(kThreads, HC > 1 ? 5 : 8) gather_kernel(const __grid_constant__ GatherParams p) {
+  constexpr unsigned kGroups = kThreads / LPR;
+  const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR, c = lane * 8;
+  const unsigned rounds = p.rounds + (blockIdx.x < p.rounds_more ? 1 : 0);
+  const unsigned round0 = blockIdx.x * p.rounds + min(blockIdx.x, p.rounds_more);
+  unsigned chunk = round0 % p.chunks, t = round0 / p.chunks * kGroups + group;
+  const int dc = p.map.dc, Hkv = p.map.Hkv;
+  const long long head_rows = 1LL << p.map.page_log2, head_codes = head_rows * dc;
+  int seq = 0, seq_first = 0, seq_end = -1, seq_base = 0;  // the sequence last looked up, and its position of token 0
+  const uint8_t* kcodes = nullptr;  // of the token last looked up, head 0
+  const uint8_t* vcodes = nullptr;
+  const float* scales = nullptr;    // this lane's: of K or of V
+  bool ok = false;
+  const auto look_up = [&] {
+    ok = false;
+    if (t >= (unsigned)p.T) return;
+    if ((int)t < seq_first || (int)t >= seq_end) {
+      int count = 0;
+      const bool found = find_sequence(p.cu, p.B, (int)t, p.T, &seq, &seq_first, &count);
+      seq_end = found ? seq_first + count : -1;
+      if (!found) return;
+      seq_base = (p.starts ? p.starts[seq] : 0) - seq_first;
     }
+    const int pos = seq_base + (int)t, page = page_of(p.map, seq, pos);
+    if (page < 0) return;
+    const long long row = p.map.row(page, 0, pos);
+    kcodes = reinterpret_cast<const uint8_t*>(p.map.k8) + row * dc + c, vcodes = p.map.v8 + row * dc + c;
+    scales = (lane < HC ? p.map.ks : p.map.vs) + row;
+    ok = true;
+  };
+  look_up();
+  uint2 kraw[HC], vraw[HC];
+  float scale;
+  const auto load_item = [&] {
+    const int h0 = (int)chunk * HC;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t w = (&kc.x)[2 * q + (e >> 1)] >> (16 * (e & 1));
-      x[e] = mul2(make_float2((float)(int)(signed char)w, (float)(int)(signed char)(w >> 8)), make_float2(ks, ks));
-      if (p.k_mean) x[e] = make_float2(__fadd_rn(x[e].x, m[2 * e]), __fadd_rn(x[e].y, m[2 * e + 1]));
+    for (int i = 0; i < HC; ++i) {
+      const bool in = ok && c < dc && (HC == 1 || h0 + i < Hkv);
+      kraw[i] = in ? *reinterpret_cast<const uint2*>(kcodes + (h0 + i) * head_codes) : make_uint2(0, 0);
+      vraw[i] = in ? *reinterpret_cast<const uint2*>(vcodes + (h0 + i) * head_codes) : make_uint2(0, 0);
     }
-    store8<T, VEC ? kWide : kScalar>(ko, c, c + 4, p.d, x, p.x_k_out);
+    const int h = h0 + lane % HC;
+    scale = ok && lane < 2 * HC && h < Hkv ? scales[h * head_rows] : 0.f;
+  };
+  load_item();
+
+#pragma unroll 1
+  for (unsigned round = 0; round < rounds; ++round) {
+    uint2 kc[HC], vc[HC];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t w = (&vc.x)[2 * q + (e >> 1)] >> (16 * (e & 1));
-      const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
-      x[e] = mul2(__half22float2(*reinterpret_cast<const __half2*>(&r)), make_float2(vs, vs));
+    for (int i = 0; i < HC; ++i) kc[i] = kraw[i], vc[i] = vraw[i];
+    const float sc = scale;
+    const bool live = ok;
+    const int h0 = (int)chunk * HC;
+    const long long out = ((long long)t * Hkv + h0) * p.d;
+    if (++chunk == p.chunks) chunk = 0, t += kGroups, look_up();
+    load_item();
+#pragma unroll
+    for (int i = 0; i < HC; ++i) {
+      const float ks = __shfl_sync(0xffffffffu, sc, i, LPR), vs = __shfl_sync(0xffffffffu, sc, HC + i, LPR);
+      if (!live || (HC > 1 && h0 + i >= Hkv)) continue;
+      float2 x[4], y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t kw = (e < 2 ? kc[i].x : kc[i].y) >> (16 * (e & 1)), vw = (e < 2 ? vc[i].x : vc[i].y) >> (16 * (e & 1));
+        x[e] = mul2(make_float2((float)(int)(signed char)kw, (float)(int)(signed char)(kw >> 8)), make_float2(ks, ks));
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)vw, __NV_E4M3);
+        y[e] = mul2(__half22float2(*reinterpret_cast<const __half2*>(&r)), make_float2(vs, vs));
+      }
+      if (p.k_mean) {
+        const float* mean = p.k_mean + (h0 + i) * p.d;
+        float m[8];
+        load4_param(mean, SAGE_FP32, p.vec_mean, c, p.d, m);
+        load4_param(mean, SAGE_FP32, p.vec_mean, c + 4, p.d, m + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = make_float2(__fadd_rn(x[e].x, m[2 * e]), __fadd_rn(x[e].y, m[2 * e + 1]));
+      }
+      const long long at = out + i * p.d;
+      store8<T, VEC ? kWide : kScalar>(static_cast<unsigned short*>(p.k_out) + at, c, c + 4, p.d, x, p.x_k_out);
+      store8<T, VEC ? kWide : kScalar>(static_cast<unsigned short*>(p.v_out) + at, c, c + 4, p.d, y, p.x_v_out);
     }
-    store8<T, VEC ? kWide : kScalar>(vo, c, c + 4, p.d, x, p.x_v_out);
   }
 }
 
 template <typename T, int LPR, int HC, int MODE>
 cudaError_t launch_rows(HeadRowsParams p, cudaStream_t st) {
   constexpr long long kGroups = kThreads / LPR;
-  const unsigned most = 148 * (HC > 1 ? 5 : 8);  // one wave
+  const unsigned most = 148 * (HC > 1 ? (p.append ? 5 : 6) : 8);  // one wave
+  const auto rounds_of = [&](const HeadRows& k) { return (unsigned)((p.tokens + kGroups - 1) / kGroups * k.chunks); };
   unsigned all = 0;
-  const auto rounds_of = [&](const HeadRows& k) { return (unsigned)((k.items + kGroups - 1) / kGroups); };
   for (const HeadRows& k : p.kind) all += rounds_of(k);
   p.apart = all <= most;
   unsigned grid = 0;
@@ -554,20 +616,14 @@ cudaError_t launch_rows(HeadRowsParams p, cudaStream_t st) {
     const unsigned rounds = rounds_of(k);
     k.ctas = p.apart ? rounds : most;
     grid = p.apart ? grid + k.ctas : most;
-    if (!k.ctas) continue;
-    k.rounds = rounds / k.ctas, k.rounds_more = rounds % k.ctas;
     if (!rounds) continue;
-    // mixed-radix step of kGroups items, and what the addresses move by
-    const long long r0 = p.token_fast ? p.N : k.chunks, r1 = p.token_fast ? k.chunks : p.N;
-    k.step[0] = (unsigned)(kGroups % r0), k.step[1] = (unsigned)(kGroups / r0 % r1);
-    k.step[2] = (unsigned)(kGroups / r0 / r1);
-    const auto moves = [&](const HeadView& v, long long* step, long long* carry) {
-      const long long s0 = p.token_fast ? v.token : v.head * HC, s1 = p.token_fast ? v.head * HC : v.token;
-      *step = k.step[0] * s0 + k.step[1] * s1 + k.step[2] * v.batch;
-      carry[0] = s1 - r0 * s0, carry[1] = v.batch - r1 * s1;
+    k.rounds = rounds / k.ctas, k.rounds_more = rounds % k.ctas;
+    // what the addresses move by: to the next chunk, and from the last one to the group's next token
+    const auto moves = [&](const HeadView& v, long long* to_chunk, long long* to_token) {
+      *to_chunk = v.head * HC, *to_token = kGroups * v.token - (k.chunks - 1) * *to_chunk;
     };
-    moves(k.in, &k.in_step, k.in_carry);
-    moves(k.out, &k.out_step, k.out_carry);
+    moves(k.in, &k.in_chunk, &k.in_tokens);
+    moves(k.out, &k.out_chunk, &k.out_tokens);
   }
   if (p.append)
     head_rows_kernel<T, LPR, HC, MODE, true><<<grid, kThreads, 0, st>>>(p);
@@ -590,21 +646,27 @@ cudaError_t launch_rows_t(const HeadRowsParams& p, cudaStream_t st) {
                                                                : launch_rows_lpr<T, 32>(p, st);
 }
 
+template <typename T, int LPR, int HC, bool VEC>
+cudaError_t launch_gather(GatherParams p, cudaStream_t st) {
+  constexpr long long kGroups = kThreads / LPR;
+  p.chunks = (p.map.Hkv + HC - 1) / HC;
+  const long long rounds = (p.T + kGroups - 1) / kGroups * p.chunks;
+  const unsigned grid = (unsigned)std::min<long long>(rounds, 148 * (HC > 1 ? 5 : 8));  // one wave
+  p.rounds = (unsigned)(rounds / grid), p.rounds_more = (unsigned)(rounds % grid);
+  gather_kernel<T, LPR, HC, VEC><<<grid, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename T, int LPR>
 cudaError_t launch_gather_lpr(const GatherParams& p, cudaStream_t st) {
-  constexpr int kGroups = kThreads / LPR;
-  const unsigned grid = (unsigned)((p.items + kGroups - 1) / kGroups);
-  if (p.vec)
-    gather_kernel<T, LPR, true><<<grid, kThreads, 0, st>>>(p);
-  else
-    gather_kernel<T, LPR, false><<<grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  if (!p.vec) return launch_gather<T, LPR, 1, false>(p, st);
+  return p.heads_per_group == 4 ? launch_gather<T, LPR, 4, true>(p, st) : launch_gather<T, LPR, 1, true>(p, st);
 }
 
 template <typename T>
 cudaError_t launch_gather_t(const GatherParams& p, cudaStream_t st) {
-  return p.d <= 64 ? launch_gather_lpr<T, 4>(p, st) : p.d <= 128 ? launch_gather_lpr<T, 8>(p, st)
-                                                                 : launch_gather_lpr<T, 16>(p, st);
+  return p.d <= 64 ? launch_gather_lpr<T, 8>(p, st) : p.d <= 128 ? launch_gather_lpr<T, 16>(p, st)
+                                                                 : launch_gather_lpr<T, 32>(p, st);
 }
 
 }  // namespace

@@ -177,11 +177,10 @@ struct HeadRows {
   const void* weight;  // [d] or nullptr
   int H;
   Extent x_out;
-  // launch shape: items of `heads_per_group` heads of one token, shared out over `ctas` CTAs in rounds of their
-  // groups (one round more for the first `rounds_more`).  An item's digits are (fastest first) token and chunk of
-  // heads, or chunk and token, then batch.
-  unsigned chunks, items, ctas, rounds, rounds_more, step[3];
-  long long in_step, in_carry[2], out_step, out_carry[2];  // what the addresses move by, and at the digits' carries
+  // launch shape: rounds (a chunk of `heads_per_group` heads of a few tokens) shared out over `ctas` CTAs, one round
+  // more for the first `rounds_more`
+  unsigned chunks, ctas, rounds, rounds_more;
+  long long in_chunk, in_tokens, out_chunk, out_tokens;  // what the addresses move by from round to round
 };
 
 struct HeadRowsParams {
@@ -200,8 +199,8 @@ struct HeadRowsParams {
   const float* k_mean;      // [Hkv][d] or nullptr
   PageMap map;
   int heads_per_group;
+  unsigned tokens; // B N (append: N)
   int apart;       // each kind has CTAs of its own (else every CTA takes a share of each)
-  int token_fast;  // consecutive groups take consecutive tokens (else consecutive heads of one token)
   bool vec, vec_weight, vec_mean;
   Extent x_k8, x_ks, x_v8, x_vs;
 };
@@ -214,7 +213,8 @@ struct GatherParams {
   void* k_out;  // [tokens][Hkv][d]
   void* v_out;
   int B, T, d;
-  long long items;  // T x Hkv
+  int heads_per_group;
+  unsigned chunks, rounds, rounds_more;  // launch shape, as of HeadRows
   bool vec, vec_mean;
   Extent x_k_out, x_v_out;
 };
