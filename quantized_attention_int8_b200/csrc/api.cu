@@ -729,9 +729,8 @@ sage_status shape_rows(HeadRowsParams* p, int batches) {
     return n;
   };
   p->heads_per_group = rows_per_group(p->vec, p->d, items(4));
-  if (items(p->heads_per_group) > kMaxItems) return SAGE_ERR_INVALID_ARG;
+  if (items(1) > kMaxItems) return SAGE_ERR_INVALID_ARG;
   p->tokens = (unsigned)tokens;
-  for (HeadRows& k : p->kind) k.chunks = (k.H + p->heads_per_group - 1) / p->heads_per_group;
   return SAGE_OK;
 }
 

@@ -166,15 +166,24 @@ __device__ __forceinline__ void load4_param(const void* src, int dtype, bool vec
   }
 }
 
-// Sums or maxima (NaN if any is one) over the LPR lanes of HC rows, one value per lane and row.  HC = 1: every
-// lane gets its row's.  HC = 4: lane l gets row 2 (l & 1) + (l >> 1 & 1)'s, by halving the values with the first two
-// exchanges: five shuffles for 16 lanes where row by row takes sixteen, and what follows from the
-// sum (a root, a division) is then done once, not four times.
+// Sums or maxima (NaN if any is one) over the LPR lanes of HC rows, one value per lane and row.  Lane l gets that of
+// row_of_lane, by halving the values with the first exchanges: for four rows five shuffles of 16 lanes where
+// row by row takes sixteen, and what follows from the sum (a root, a division) is done once, not four
+// times.
+template <int HC>
+__device__ __forceinline__ int row_of_lane(int lane) {
+  return HC == 1 ? 0 : HC == 2 ? (lane & 1) : 2 * (lane & 1) + (lane >> 1 & 1);
+}
 template <int LPR, int HC, bool MAX>
 __device__ __forceinline__ float reduce_rows(const float (&v)[HC]) {
   const auto op = [](float a, float b) { return MAX ? max_nan(a, b) : a + b; };
   float r = v[0];
   int from = 1;
+  if (HC == 2) {
+    const bool b0 = threadIdx.x & 1;
+    r = op(b0 ? v[1 % HC] : v[0], __shfl_xor_sync(0xffffffffu, b0 ? v[0] : v[1 % HC], 1));
+    from = 2;
+  }
   if (HC == 4) {
     const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
     const float u0 = op(b0 ? v[2 % HC] : v[0], __shfl_xor_sync(0xffffffffu, b0 ? v[0] : v[2 % HC], 1));
@@ -190,7 +199,7 @@ __device__ __forceinline__ float reduce_rows(const float (&v)[HC]) {
 // Row i's value of what reduce_rows left in the lanes, to all of them.
 template <int LPR, int HC>
 __device__ __forceinline__ float of_row(float v, int i) {
-  return HC == 1 ? v : __shfl_sync(0xffffffffu, v, (i >> 1) | (i & 1) << 1, LPR);
+  return HC == 1 ? v : __shfl_sync(0xffffffffu, v, HC == 2 ? i : (i >> 1) | (i & 1) << 1, LPR);
 }
 
 // scale and reciprocal of a row's codes: 0 and 0 for a row of (almost) zeros, NaN and 0 for one
@@ -261,6 +270,11 @@ __device__ __forceinline__ uint32_t code4_e4m3(float2 x, float2 y, float2 inv) {
 
 enum RowKind { kQ = 0, kK = 1, kV = 2 };
 
+// Heads that a group takes at a time.  Four; coded keys two, whose fp32 rows stay in registers from the amax to the
+// codes: with four, 96 registers, spills and five CTAs to an SM, the write of four 8192-token prompts took 169
+// us, with two and six CTAs 160.
+__host__ __device__ constexpr int heads_at_a_time(int hc, bool append, int kind) { return append && kind == kK && hc == 4 ? 2 : hc; }
+
 // The rows of one kind.  An item: HC heads of one token, taken by one group of LPR lanes.  The cosines, the
 // weights and the token's place are fetched once for all of them, and the heads of a group's next item
 // are loaded while it works on this one: without that, 24 warps to an SM spend most of their time
@@ -319,7 +333,7 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
   const float* angles = p.cos_sin;  // (groups without an item read row 0 as well)
   uint8_t* codes = nullptr;
   float* scales = nullptr;
-  const long long head_rows = 1LL << p.map.page_log2, head_codes = head_rows * p.map.dc;
+  const unsigned head_rows = 1u << p.map.page_log2, head_codes = head_rows * p.map.dc;  // of a page
 
   // Every lane of a warp makes the same number of rounds: the shuffles need them all.
 #pragma unroll 1
@@ -485,7 +499,7 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
       uint32_t w1 = KIND == kK ? code4_int8(x[2], x[3], inv2) : code4_e4m3(x[2], x[3], inv2);
       if (odd && iv == 0.f) w0 = w1 = 0;
       if (live && (HC == 1 || h0 + i < k.H)) {
-        uint8_t* const code = codes + (h0 + i) * head_codes;
+        uint8_t* const code = codes + (unsigned long long)(unsigned)(h0 + i) * head_codes;
         const Extent& xc = KIND == kK ? p.x_k8 : p.x_v8;
         if (MODE == kHalves) {
           if (a < p.map.dc && SAGE_STORE_OK(xc, code + a, 4, &g_cache_error)) *reinterpret_cast<uint32_t*>(code + a) = w0;
@@ -495,8 +509,8 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
         }
       }
     }
-    const int my_row = HC == 1 ? 0 : 2 * (lane & 1) + (lane >> 1 & 1);
-    float* sdst = scales + (h0 + my_row) * head_rows;
+    const int my_row = row_of_lane<HC>(lane);
+    float* sdst = scales + (unsigned long long)(unsigned)(h0 + my_row) * head_rows;
     if (lane < HC && live && h0 + my_row < k.H && SAGE_STORE_OK(KIND == kK ? p.x_ks : p.x_vs, sdst, 4, &g_cache_error))
       *sdst = scale;
   }
@@ -505,11 +519,11 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
 // Large calls: every CTA takes its share of each kind, one after the other, so that all end together
 // whatever a kind's rows cost.  Small ones (`apart`): the kinds have CTAs of their own, which work at the same time.
 template <typename T, int LPR, int HC, int MODE, bool APPEND>
-__global__ void __launch_bounds__(kThreads, HC > 1 ? (APPEND ? 5 : 6) : 8) head_rows_kernel(const __grid_constant__ HeadRowsParams p) {
+__global__ void __launch_bounds__(kThreads, HC > 1 ? 6 : 8) head_rows_kernel(const __grid_constant__ HeadRowsParams p) {
   __shared__ float partner_buf[MODE == kScalar ? kThreads * 8 : 1];
   const unsigned cta = blockIdx.x, q = p.apart ? p.kind[kQ].ctas : 0, k = p.apart ? q + p.kind[kK].ctas : 0;
   if (!p.apart || cta < q) head_rows<T, LPR, HC, MODE, APPEND, kQ>(p, p.kind[kQ], cta, partner_buf);
-  if (!p.apart || (cta >= q && cta < k)) head_rows<T, LPR, HC, MODE, APPEND, kK>(p, p.kind[kK], cta - q, partner_buf);
+  if (!p.apart || (cta >= q && cta < k)) head_rows<T, LPR, heads_at_a_time(HC, APPEND, kK), MODE, APPEND, kK>(p, p.kind[kK], cta - q, partner_buf);
   if (APPEND && (!p.apart || cta >= k))
     head_rows<T, LPR, HC, MODE == kHalves ? kWide : MODE, APPEND, kV>(p, p.kind[kV], cta - k, partner_buf);
 }
@@ -526,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, HC > 1 ? 5 : 8) gather_kernel(const 
   const unsigned round0 = blockIdx.x * p.rounds + min(blockIdx.x, p.rounds_more);
   unsigned chunk = round0 % p.chunks, t = round0 / p.chunks * kGroups + group;
   const int dc = p.map.dc, Hkv = p.map.Hkv;
-  const long long head_rows = 1LL << p.map.page_log2, head_codes = head_rows * dc;
+  const unsigned head_rows = 1u << p.map.page_log2, head_codes = head_rows * dc;  // of a page
   int seq = 0, seq_first = 0, seq_end = -1, seq_base = 0;  // the sequence last looked up, and its position of token 0
   const uint8_t* kcodes = nullptr;  // of the token last looked up, head 0
   const uint8_t* vcodes = nullptr;
@@ -557,11 +571,12 @@ __global__ void __launch_bounds__(kThreads, HC > 1 ? 5 : 8) gather_kernel(const 
 #pragma unroll
     for (int i = 0; i < HC; ++i) {
       const bool in = ok && c < dc && (HC == 1 || h0 + i < Hkv);
-      kraw[i] = in ? *reinterpret_cast<const uint2*>(kcodes + (h0 + i) * head_codes) : make_uint2(0, 0);
-      vraw[i] = in ? *reinterpret_cast<const uint2*>(vcodes + (h0 + i) * head_codes) : make_uint2(0, 0);
+      const unsigned long long at = (unsigned long long)(unsigned)(h0 + i) * head_codes;
+      kraw[i] = in ? *reinterpret_cast<const uint2*>(kcodes + at) : make_uint2(0, 0);
+      vraw[i] = in ? *reinterpret_cast<const uint2*>(vcodes + at) : make_uint2(0, 0);
     }
     const int h = h0 + lane % HC;
-    scale = ok && lane < 2 * HC && h < Hkv ? scales[h * head_rows] : 0.f;
+    scale = ok && lane < 2 * HC && h < Hkv ? scales[(unsigned long long)(unsigned)h * head_rows] : 0.f;
   };
   load_item();
 
@@ -606,10 +621,11 @@ __global__ void __launch_bounds__(kThreads, HC > 1 ? 5 : 8) gather_kernel(const 
 template <typename T, int LPR, int HC, int MODE>
 cudaError_t launch_rows(HeadRowsParams p, cudaStream_t st) {
   constexpr long long kGroups = kThreads / LPR;
-  const unsigned most = 148 * (HC > 1 ? (p.append ? 5 : 6) : 8);  // one wave
+  const unsigned most = 148 * (HC > 1 ? 6 : 8);  // one wave
   const auto rounds_of = [&](const HeadRows& k) { return (unsigned)((p.tokens + kGroups - 1) / kGroups * k.chunks); };
   unsigned all = 0;
-  for (const HeadRows& k : p.kind) all += rounds_of(k);
+  const auto heads = [&](const HeadRows& k) { return heads_at_a_time(HC, p.append, (int)(&k - p.kind)); };
+  for (HeadRows& k : p.kind) k.chunks = (k.H + heads(k) - 1) / heads(k), all += rounds_of(k);
   p.apart = all <= most;
   unsigned grid = 0;
   for (HeadRows& k : p.kind) {
@@ -620,7 +636,7 @@ cudaError_t launch_rows(HeadRowsParams p, cudaStream_t st) {
     k.rounds = rounds / k.ctas, k.rounds_more = rounds % k.ctas;
     // what the addresses move by: to the next chunk, and from the last one to the group's next token
     const auto moves = [&](const HeadView& v, long long* to_chunk, long long* to_token) {
-      *to_chunk = v.head * HC, *to_token = kGroups * v.token - (k.chunks - 1) * *to_chunk;
+      *to_chunk = v.head * heads(k), *to_token = kGroups * v.token - (k.chunks - 1) * *to_chunk;
     };
     moves(k.in, &k.in_chunk, &k.in_tokens);
     moves(k.out, &k.out_chunk, &k.out_tokens);

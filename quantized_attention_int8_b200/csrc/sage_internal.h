@@ -177,7 +177,7 @@ struct HeadRows {
   const void* weight;  // [d] or nullptr
   int H;
   Extent x_out;
-  // launch shape: rounds (a chunk of `heads_per_group` heads of a few tokens) shared out over `ctas` CTAs, one round
+  // launch shape: rounds (a chunk of heads of a few tokens) shared out over `ctas` CTAs, one round
   // more for the first `rounds_more`
   unsigned chunks, ctas, rounds, rounds_more;
   long long in_chunk, in_tokens, out_chunk, out_tokens;  // what the addresses move by from round to round
