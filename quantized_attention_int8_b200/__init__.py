@@ -21,6 +21,7 @@ optional V smoothing (see ``sage_opts`` in include/sage.h).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -28,7 +29,7 @@ import torch
 __all__ = [
     "SageError", "sage_attn", "sage_quantize", "sage_attn_quantized", "sage_qk_int32", "sage_check_status",
     "sage_workspace_bytes", "sage_device_supported", "sage_status_string", "padded_dim", "LIB_PATH", "capi",
-    "sage_attn_noalloc", "SAGE_NOALLOC_MAX_BYTES", "load_checked", "CHECKED_LIB_PATH", "pv_mode", "sage_attn_varlen", "SageOpts", "opts",
+    "sage_attn_noalloc", "SAGE_NOALLOC_MAX_BYTES", "load_checked", "CHECKED_LIB_PATH", "BINDING_PATH", "pv_mode", "sage_attn_varlen", "SageOpts", "opts",
     "sage_qk_norm_rope", "sage_kv_cache", "sage_cache_append", "sage_cache_gather", "sage_attn_decode",
     "sageattn", "sageattn_qk_int8_pv_fp8_cuda", "sageattn_qk_int8_pv_fp16_cuda", "sageattn_varlen",
 ]
@@ -36,6 +37,9 @@ __all__ = [
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsage_b200.so")
 # the same library compiled with -DSAGE_CHECKED: every kernel store tests its extent first
 CHECKED_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsage_b200_checked.so")
+
+# the compiled binding of the serving calls (csrc/binding.cpp)
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_sage_binding.so")
 
 SAGE_OK, SAGE_ERR_INVALID_ARG, SAGE_ERR_UNSUPPORTED, SAGE_ERR_ARCH, SAGE_ERR_CUDA, SAGE_ERR_OOM, \
     SAGE_ERR_TIMEOUT, SAGE_ERR_BOUNDS = range(8)
@@ -128,10 +132,23 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, res
+    # the addresses that the compiled binding of the serving calls takes
+    lib.serving = {name: ctypes.cast(getattr(lib, name), P).value
+                   for name in ("sage_qk_norm_rope", "sage_cache_append", "sage_cache_gather", "sage_attn_decode")}
     return lib
 
 
+def _load_binding(path: str = BINDING_PATH):
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built; run `python quantized_attention_int8_b200/build_lib.py`")
+    spec = importlib.util.spec_from_file_location("_sage_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
 capi = _load()
+_binding = _load_binding()
 
 
 def load_checked() -> ctypes.CDLL:
@@ -292,104 +309,10 @@ def sage_attn_noalloc(q, k, v, tensor_layout="HND", is_causal=False, sm_scale=No
 
 # ---------------------------------------------------------------------------------------------
 # Serving: head norm and rotation, the paged cache, one-token attention (include/sage.h, "Serving").
-# None of these record gradients.
+# None of these record gradients.  They go through a compiled binding (csrc/binding.cpp), which checks the
+# tensors, allocates the outputs and calls the same C functions: at a decode step's sizes the checks and
+# conversions took longer in Python than the kernels.
 # ---------------------------------------------------------------------------------------------
-# The current stream's handle, without building a torch.cuda.Stream for it (3 us of a decode step's call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _call(dev, name, *args):
-    """One C entry point on device ``dev`` (an index) and its current stream."""
-    if dev == torch.cuda.current_device():
-        st = getattr(capi, name)(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = getattr(capi, name)(*args, _raw_stream(dev))
-    if st != SAGE_OK:
-        _check(st, name)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _check_heads(name, t, dtype=None, dev=None):
-    """Strides of a CUDA tensor of heads with contiguous channels, of this dtype and on this device (an index)."""
-    if t.get_device() < 0:
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
-    if dtype is not None and (t.dtype != dtype or t.get_device() != dev):
-        raise ValueError(f"{name} must have dtype {dtype} and be on cuda:{dev}, got {t.dtype} on {t.device}")
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1 and t.numel():
-        raise ValueError(f"the channels (last dimension) of {name} must be contiguous")
-    return st
-
-
-def _check_out(name, t, like, dev):
-    if t.shape != like.shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
-    return _check_heads(name, t, like.dtype, dev)
-
-
-def _check_ints(name, t, shape, dev):
-    """An int32 CUDA tensor of this shape (None: any extent) whose last dimension is contiguous."""
-    s = t.shape
-    if t.dtype is not torch.int32 or t.get_device() != dev or len(s) != len(shape):
-        raise ValueError(f"{name} must be a {len(shape)}-D int32 tensor on cuda:{dev}")
-    for n, m in zip(shape, s):
-        if n is not None and n != m:
-            raise ValueError(f"{name} has shape {tuple(s)}, expected {shape}")
-    if s[-1] > 1 and t.stride()[-1] != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-
-
-def _check_floats(name, t, shape, dev):
-    if t.dtype is not torch.float32 or t.get_device() != dev or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on cuda:{dev}")
-
-
-def _norm_rope(d, dev, norm, eps, q_weight, k_weight, cos_sin, interleaved) -> SageNormRope:
-    wdtype = None
-    if q_weight is not None or k_weight is not None:
-        if not norm:
-            raise ValueError("q_weight and k_weight need norm=True")
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is None:
-                continue
-            if w.get_device() != dev or w.dtype not in _DTYPES or tuple(w.shape) != (d,) or not w.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous fp16, bf16 or fp32 tensor of shape ({d},) on cuda:{dev}")
-            if wdtype is not None and w.dtype != wdtype:
-                raise ValueError("q_weight and k_weight must share one dtype")
-            wdtype = w.dtype
-    table, n_pos, rot = None, 0, 0
-    if cos_sin is not None:
-        if cos_sin.dtype is not torch.float32 or cos_sin.get_device() != dev or cos_sin.dim() != 2 \
-                or not cos_sin.is_contiguous():
-            raise ValueError(f"cos_sin must be a contiguous 2-D float32 tensor (positions, rotary_dim) on cuda:{dev}")
-        table, (n_pos, rot) = cos_sin.data_ptr(), cos_sin.shape
-    return SageNormRope(1 if norm else 0, eps, _ptr(q_weight), _ptr(k_weight),
-                        SAGE_FP32 if wdtype is None else _DTYPES[wdtype], table, n_pos, rot, 1 if interleaved else 0)
-
-
-def _btn(shape, st, layout):
-    """(batches, tokens, heads) and their element strides of a 4-D HND / NHD or a 3-D packed tensor."""
-    if len(shape) == 3:
-        return (1, shape[0], shape[1]), (0, st[0], st[1])
-    if len(shape) != 4:
-        raise ValueError("q and k must be 4-D, or 3-D (tokens, heads, head_dim)")
-    if layout == "HND":
-        return (shape[0], shape[2], shape[1]), (st[0], st[2], st[1])
-    if layout == "NHD":
-        return (shape[0], shape[1], shape[2]), (st[0], st[1], st[2])
-    raise ValueError(f"tensor_layout must be 'HND' or 'NHD', got {layout!r}")
-
-
-_Strides8, _Strides12 = ctypes.c_longlong * 8, ctypes.c_longlong * 12
-
-
 def sage_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weight=None, tensor_layout="HND", norm=True,
                       eps=1e-6, interleaved=False, q_out=None, k_out=None):
     """RMS norm of every query and key head and its position rotation in one launch; returns (q_out, k_out).
@@ -400,36 +323,13 @@ def sage_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weigh
     2i and 2i + 1 with interleaved; None: no rotation.  positions int32 (N,) or (B,N), default 0..N-1; one
     outside the table leaves its token unwritten and is reported by sage_check_status.  Weights (d,) in fp16,
     bf16 or fp32.  q_out may be q and k_out may be k."""
-    st = _check_heads("q", q)
-    shape, dev = q.shape, q.get_device()
-    (B, N, Hq), qs = _btn(shape, st, tensor_layout)
-    d = shape[-1]
-    Hkv, ks, kos = 0, (0, 0, 0), (0, 0, 0)
-    if k is not None:
-        st = _check_heads("k", k, q.dtype, dev)
-        (Bk, Nk, Hkv), ks = _btn(k.shape, st, tensor_layout)
-        if Bk != B or Nk != N or k.shape[-1] != d or len(k.shape) != len(shape):
-            raise ValueError(f"k of shape {tuple(k.shape)} does not fit q of shape {tuple(shape)}")
-        if k_out is None:
-            k_out = k.new_empty(k.shape)
-        kos = _btn(k.shape, _check_out("k_out", k_out, k, dev), tensor_layout)[1]
-    elif k_out is not None:
-        raise ValueError("k_out needs k")
-    pos_stride = 0
-    if positions is not None:
-        if cos_sin is None:
-            raise ValueError("positions need cos_sin")
-        one = positions.dim() == 1
-        _check_ints("positions", positions, (N,) if one else (B, N), dev)
-        pos_stride = 0 if one else positions.stride(0)
-    if q_out is None:
-        q_out = q.new_empty(shape)
-    qos = _btn(shape, _check_out("q_out", q_out, q, dev), tensor_layout)[1]
-    nr = _norm_rope(d, dev, norm, eps, q_weight, k_weight, cos_sin, interleaved)
-    _call(dev, "sage_qk_norm_rope", q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out),
-          _Strides12(*qs, *ks, *qos, *kos), _ptr(positions), pos_stride, B, N, Hq, Hkv, d, _DTYPES[q.dtype],
-          ctypes.byref(nr))
-    return q_out, k_out
+    if tensor_layout not in _LAYOUTS:
+        raise ValueError(f"tensor_layout must be 'HND' or 'NHD', got {tensor_layout!r}")
+    r = _binding.qk_norm_rope(capi.serving["sage_qk_norm_rope"], q, k, positions, tensor_layout == "HND", cos_sin,
+                              q_weight, k_weight, norm, eps, interleaved, q_out, k_out)
+    if type(r) is int:
+        _check(r, "sage_qk_norm_rope")
+    return r
 
 
 def sage_kv_cache(num_pages, num_kv_heads, head_dim, page_size=64, device="cuda") -> dict:
@@ -443,22 +343,6 @@ def sage_kv_cache(num_pages, num_kv_heads, head_dim, page_size=64, device="cuda"
                 vs=torch.zeros(shape, dtype=torch.float32, device=device))
 
 
-def _cache_struct(cache, d, dev) -> SageKVCache:
-    k8, ks, v8, vs = cache["k8"], cache["ks"], cache["v8"], cache["vs"]
-    if k8.dtype is not torch.int8 or v8.dtype is not torch.uint8 or ks.dtype is not torch.float32 \
-            or vs.dtype is not torch.float32:
-        raise ValueError("the cache holds k8 int8, v8 uint8, ks and vs float32")
-    for t in (k8, ks, v8, vs):
-        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
-            raise ValueError(f"the cache's arrays must be contiguous CUDA tensors on one device (cuda:{dev})")
-    shape = k8.shape
-    if len(shape) != 4 or shape[3] != (d + 15) // 16 * 16:
-        raise ValueError(f"cache['k8'] of shape {tuple(shape)} does not hold heads of {d} channels")
-    if v8.shape != shape or ks.shape != shape[:3] or vs.shape != shape[:3]:
-        raise ValueError("the cache's arrays do not fit one another")
-    return SageKVCache(k8.data_ptr(), ks.data_ptr(), v8.data_ptr(), vs.data_ptr(), shape[0], shape[2], shape[1], d)
-
-
 def sage_cache_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, q=None, cos_sin=None, q_weight=None,
                       k_weight=None, norm=False, eps=1e-6, interleaved=False, k_mean=None, q_out=None):
     """Quantizes new tokens k, v (T,Hkv,d) into the paged cache (a dict as sage_kv_cache returns).
@@ -469,41 +353,12 @@ def sage_cache_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, q=None
     which is returned (q_out; None without q).  k_mean float32 (Hkv,d) is subtracted from the keys before
     they are coded.  Channels contiguous, other strides free.  Bad pages and positions are skipped and reported
     by sage_check_status."""
-    kst = _check_heads("k", k)
-    dtype, dev, shape = k.dtype, k.get_device(), k.shape
-    vst = _check_heads("v", v, dtype, dev)
-    if len(shape) != 3 or v.shape != shape:
-        raise ValueError("k and v must be 3-D (tokens, heads, head_dim) and of one shape")
-    T, Hkv, d = shape
-    c = _cache_struct(cache, d, dev)
-    if c.Hkv != Hkv:
-        raise ValueError(f"the cache has {c.Hkv} heads, k {Hkv}")
-    _check_ints("page_table", page_table, (None, None), dev)
-    B, max_pages = page_table.shape
-    _check_ints("seq_lens", seq_lens, (B,), dev)
-    if cu_seqlens is not None:
-        _check_ints("cu_seqlens", cu_seqlens, (B + 1,), dev)
-    elif T != B:
-        raise ValueError(f"{T} tokens for {B} sequences: pass cu_seqlens")
-    if k_mean is not None:
-        _check_floats("k_mean", k_mean, (Hkv, d), dev)
-    Hq, qst, qost = 0, (0, 0), (0, 0)
-    if q is not None:
-        qst = _check_heads("q", q, dtype, dev)
-        if len(q.shape) != 3 or q.shape[0] != T or q.shape[2] != d:
-            raise ValueError(f"q of shape {tuple(q.shape)} does not fit k of shape {tuple(shape)}")
-        Hq = q.shape[1]
-        if q_out is None:
-            q_out = q.new_empty(q.shape)
-        qost = _check_out("q_out", q_out, q, dev)
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    nr = _norm_rope(d, dev, norm, eps, q_weight, k_weight, cos_sin, interleaved)
-    _call(dev, "sage_cache_append", ctypes.byref(c), _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out),
-          _Strides8(qst[0], qst[1], kst[0], kst[1], vst[0], vst[1], qost[0], qost[1]), page_table.data_ptr(),
-          page_table.stride(0), max_pages, seq_lens.data_ptr(), _ptr(cu_seqlens), _ptr(k_mean), T, B, Hq,
-          _DTYPES[dtype], ctypes.byref(nr))
-    return q_out
+    r = _binding.cache_append(capi.serving["sage_cache_append"], cache["k8"], cache["ks"], cache["v8"], cache["vs"], k, v,
+                              page_table, seq_lens, cu_seqlens, q, cos_sin, q_weight, k_weight, norm, eps, interleaved,
+                              k_mean, q_out)
+    if type(r) is int:
+        _check(r, "sage_cache_append")
+    return r
 
 
 def sage_cache_gather(cache, page_table, cu_seqlens, total, head_dim, dtype=torch.float16, starts=None, k_mean=None,
@@ -511,32 +366,14 @@ def sage_cache_gather(cache, page_table, cu_seqlens, total, head_dim, dtype=torc
     """Reads cached tokens back as (k, v), each (total, Hkv, head_dim) of ``dtype``: token i of sequence b (rows
     cu_seqlens[b] .. cu_seqlens[b+1]-1) is position starts[b] + i (starts None: 0).  k_mean is added to the keys.
     Rows behind the last sequence, and rows of bad pages, are left unwritten."""
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise ValueError(f"unsupported dtype {dtype}")
-    k8 = cache["k8"]
-    dev = k8.get_device()
-    c = _cache_struct(cache, head_dim, dev)
-    _check_ints("page_table", page_table, (None, None), dev)
-    B, max_pages = page_table.shape
-    _check_ints("cu_seqlens", cu_seqlens, (B + 1,), dev)
-    if starts is not None:
-        _check_ints("starts", starts, (B,), dev)
-    if k_mean is not None:
-        _check_floats("k_mean", k_mean, (c.Hkv, head_dim), dev)
-    total = int(total)
-    shape = (total, c.Hkv, head_dim)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None and (t.get_device() != dev or t.dtype != dtype or tuple(t.shape) != shape
-                              or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on cuda:{dev}")
-    if k_out is None:
-        k_out = k8.new_empty(shape, dtype=dtype)
-    if v_out is None:
-        v_out = k8.new_empty(shape, dtype=dtype)
-    _call(dev, "sage_cache_gather", ctypes.byref(c), page_table.data_ptr(), page_table.stride(0), max_pages,
-          cu_seqlens.data_ptr(), _ptr(starts), _ptr(k_mean), k_out.data_ptr(), v_out.data_ptr(), total, B,
-          _DTYPES[dtype])
-    return k_out, v_out
+    r = _binding.cache_gather(capi.serving["sage_cache_gather"], cache["k8"], cache["ks"], cache["v8"], cache["vs"],
+                              page_table, cu_seqlens, total, head_dim, code, starts, k_mean, k_out, v_out)
+    if type(r) is int:
+        _check(r, "sage_cache_gather")
+    return r
 
 
 def sage_attn_decode(q, cache, page_table, seq_lens, max_seqlen, sm_scale=None, out=None):
@@ -544,24 +381,11 @@ def sage_attn_decode(q, cache, page_table, seq_lens, max_seqlen, sm_scale=None, 
 
     seq_lens int32 (B,): the cached keys each query sees (0: zeros); max_seqlen bounds them (a longer sequence gets
     zeros and is reported by sage_check_status).  q may be strided (channels contiguous)."""
-    st = _check_heads("q", q)
-    shape, dev = q.shape, q.get_device()
-    if len(shape) != 3:
-        raise ValueError("q must be 3-D (sequences, heads, head_dim)")
-    B, Hq, d = shape
-    c = _cache_struct(cache, d, dev)
-    _check_ints("page_table", page_table, (B, None), dev)
-    _check_ints("seq_lens", seq_lens, (B,), dev)
-    if out is None:
-        out = q.new_empty(shape)
-    else:
-        _check_out("out", out, q, dev)
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous")
-    _call(dev, "sage_attn_decode", q.data_ptr(), st[0], st[1], ctypes.byref(c), page_table.data_ptr(),
-          page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(), out.data_ptr(), B, Hq, int(max_seqlen),
-          _DTYPES[q.dtype], 0.0 if sm_scale is None else float(sm_scale))
-    return out
+    r = _binding.attn_decode(capi.serving["sage_attn_decode"], cache["k8"], cache["ks"], cache["v8"], cache["vs"], q,
+                             page_table, seq_lens, max_seqlen, 0.0 if sm_scale is None else sm_scale, out)
+    if type(r) is int:
+        _check(r, "sage_attn_decode")
+    return r
 
 
 def sage_workspace_bytes(B, Hq, Hkv, N, d) -> int:

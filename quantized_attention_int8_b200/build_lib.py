@@ -1,5 +1,6 @@
 """Builds the CUDA library in-tree with nvcc for sm_100a: libsage_b200.so and its checked
-twin libsage_b200_checked.so (-DSAGE_CHECKED: every kernel store tests its extent first).
+twin libsage_b200_checked.so (-DSAGE_CHECKED: every kernel store tests its extent first); and
+_sage_binding.so, the serving calls' Python binding (host code against torch's headers).
 
 Usage: python quantized_attention_int8_b200/build_lib.py [--force] [--ptxas-info] [--no-checked]
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsage_b200.so")
 LIB_CHECKED = os.path.join(PKG, "libsage_b200_checked.so")
+BINDING = os.path.join(PKG, "_sage_binding.so")
 SOURCES = ["api.cu", "attn.cu", "quant.cu", "cache.cu", "decode.cu"]
 HEADERS = ["sm100.cuh", "sage_internal.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -31,16 +34,16 @@ def _nvcc() -> str:
     return cand
 
 
-def _stale(lib: str) -> bool:
+def _stale(lib: str, sources: list[str]) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "sage.h")]
+    deps = [os.path.join(CSRC, f) for f in sources] + [os.path.join(INCLUDE, "sage.h")]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
 def _build_one(lib: str, defines: list[str], force: bool, ptxas_info: bool, verbose: bool) -> str:
-    if not force and not _stale(lib):
+    if not force and not _stale(lib, SOURCES + HEADERS):
         return lib
     tmp = lib + ".tmp"
     cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-shared",
@@ -59,8 +62,30 @@ def _build_one(lib: str, defines: list[str], force: bool, ptxas_info: bool, verb
     return lib
 
 
+def _build_binding(force: bool, verbose: bool) -> None:
+    if not force and not _stale(BINDING, ["binding.cpp"]):
+        return
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           *[x for i in includes for x in ("-isystem", i)], "-o", tmp, os.path.join(CSRC, "binding.cpp"),
+           f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False, checked: bool = True) -> str:
-    """Builds the library (and, unless checked=False, its checked twin); returns the library's path."""
+    """Builds the library (and, unless checked=False, its checked twin) and the binding; returns the library's path."""
+    _build_binding(force, verbose)
     _build_one(LIB, [], force, ptxas_info, verbose)
     if checked:
         _build_one(LIB_CHECKED, ["-DSAGE_CHECKED"], force, ptxas_info, verbose)

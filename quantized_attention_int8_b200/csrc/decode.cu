@@ -175,7 +175,7 @@ __device__ __forceinline__ int seq_len_of(const DecodeParams& p, int b, bool rep
   return 0;
 }
 
-// The work, cut into units of 64 keys (more where 2^31 of those would not do) of one (sequence, kv head, tile
+// The work, cut into units of 256 keys (or more, see the launch) of one (sequence, kv head, tile
 // of heads): sequence by sequence, its pairs of kv head and head tile one after the other.  Every CTA takes
 // the same number of units, whatever the sequences' lengths, so that a ragged batch ends everywhere at
 // once; a pair that crosses CTAs is joined.
