@@ -861,17 +861,19 @@ sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long 
   p.x_out = extent_of(out, out_bytes);
   if ((s = check_device()) != SAGE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // one CTA per unit of work, but no more than run at the same time on a B200's 148 SMs
-  const auto units = [&] {
-    return (long long)B * p.pairs * std::max<long long>(1, ((long long)p.max_len + (1 << p.unit_log2) - 1) >> p.unit_log2);
+  // One CTA per unit of work, but no more than run at the same time on a B200's 148 SMs.  Units of 64 keys, so that
+  // the CTAs' shares are even.  Of 256 where that is no more units than CTAs: a sequence of 4000 keys (B1,
+  // Hq32, Hkv8, d128) then takes 15.8 us, joined from 60 parts 19.3.  Sequences of up to 512 keys are not
+  // split at all: the join takes as long as the keys that it saves a CTA (12.8 and 12.9 us at 500 keys, 14.6 and 18.4
+  // us at 1000), and a second launch and a workspace.
+  const long long most = 148LL * decode_ctas_per_sm(p.d);
+  const auto units = [&](int log2) {
+    return (long long)B * p.pairs * std::max<long long>(1, ((long long)p.max_len + (1 << log2) - 1) >> log2);
   };
-  // Units of 256 keys (of 64, that a sequence of 4000 keys is joined from 60 parts cost 3 us; measured at B1, Hq32, Hkv8,
-  // d128: 19.3 and 15.8 us).  Sequences of up to 512 keys are not split at all: the join takes as long as the
-  // keys that it saves a CTA (12.8 and 12.9 us at 500 keys, 14.6 and 18.4 us at 1000), and a launch and a workspace.
-  p.unit_log2 = p.max_len <= 512 ? 9 : 8;
-  while (units() >= (1LL << 31) && p.unit_log2 < 30) ++p.unit_log2;
-  if (units() >= (1LL << 31)) return SAGE_ERR_INVALID_ARG;
-  p.ctas = (uint32_t)std::min<long long>(units(), 148LL * decode_ctas_per_sm(p.d));
+  p.unit_log2 = p.max_len <= 512 ? 9 : units(8) <= most ? 8 : 6;
+  while (units(p.unit_log2) >= (1LL << 31) && p.unit_log2 < 30) ++p.unit_log2;
+  if (units(p.unit_log2) >= (1LL << 31)) return SAGE_ERR_INVALID_ARG;
+  p.ctas = (uint32_t)std::min<long long>(units(p.unit_log2), most);
   unsigned char* ws = nullptr;
   if (p.max_len > 1 << p.unit_log2) {  // a pair may cross CTAs
     const size_t parts = (size_t)p.ctas * 2 * kDecodeHeads;

@@ -137,12 +137,13 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity) {
 }
 
 // One warp's ring of stages in shared memory, kTiles 16-key tiles to a stage.  A tile: 16 K rows; four groups of
-// four V rows, kPad bytes apart; 16 K scales and 16 V scales.  Two tiles are worked on at a time where they
-// fit: the chain from a score to its weight is latency, and three warps to a scheduler hide little of it.
+// four V rows, kPad bytes apart; 16 K scales and 16 V scales.  Two or four tiles are worked on at a time where
+// they fit: the chain from a score to its weight is latency, and three warps to a scheduler hide little of
+// it (B32 L16384 Hq32 Hkv8: d 128 one tile 223 us, two 187; d 64 two 148 us, four 136).
 template <int DP>
 struct Ring {
-  static constexpr int kTiles = DP == 256 ? 1 : 2;
-  static constexpr int kStages = DP == 128 ? 2 : 3;
+  static constexpr int kTiles = DP == 256 ? 1 : DP == 128 ? 2 : 4;
+  static constexpr int kStages = DP == 256 ? 3 : 2;
   static constexpr int kPad = 32;
   static __host__ __device__ constexpr int v_at(int dc) { return 16 * dc; }
   static __host__ __device__ constexpr int v_group(int dc) { return 4 * dc + kPad; }
@@ -175,7 +176,7 @@ __device__ __forceinline__ int seq_len_of(const DecodeParams& p, int b, bool rep
   return 0;
 }
 
-// The work, cut into units of 256 keys (or more, see the launch) of one (sequence, kv head, tile
+// The work, cut into units of 2^unit_log2 keys (the launch says which) of one (sequence, kv head, tile
 // of heads): sequence by sequence, its pairs of kv head and head tile one after the other.  Every CTA takes
 // the same number of units, whatever the sequences' lengths, so that a ragged batch ends everywhere at
 // once; a pair that crosses CTAs is joined.
@@ -195,6 +196,13 @@ template <int NT>
 __device__ __forceinline__ Place find_place(const DecodeParams& p, uint32_t cta, bool report) {
   __shared__ uint32_t sm_sum[NT / 32];
   __shared__ Place sm_place;
+  if (!p.part_o) {  // one unit to every pair: no sum over the lengths (1 us of a short call)
+    Place at;
+    at.total = p.B * p.pairs, at.share = (at.total + p.ctas - 1) / p.ctas, at.pair0 = cta * at.share;
+    at.b = at.pair0 < at.total ? (int)(at.pair0 / p.pairs) : -1, at.pair = (int)(at.pair0 % p.pairs);
+    at.len = at.b >= 0 ? seq_len_of(p, at.b, threadIdx.x == 0) : 0;
+    return at;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.B + NT - 1) / NT, b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
   uint32_t mine = 0;
@@ -558,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
     }
     unit += n_seg, pair0 += n_pair;
     if (unit >= unit_end || sm_dead) return;
-    if (++pair == p.pairs) pair = 0, ++b, len = seq_len_of(p, b, false);
+    if (++pair == p.pairs) pair = 0, ++b, len = seq_len_of(p, b, !p.part_o && threadIdx.x == 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();  // O is read: the rings may be filled again
   }
