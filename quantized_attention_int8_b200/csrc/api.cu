@@ -861,21 +861,26 @@ sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long 
   p.x_out = extent_of(out, out_bytes);
   if ((s = check_device()) != SAGE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // One CTA per unit of work, but no more than run at the same time on a B200's 148 SMs.  Units of 64 keys, so that
-  // the CTAs' shares are even.  Of 256 where that is no more units than CTAs: a sequence of 4000 keys (B1,
-  // Hq32, Hkv8, d128) then takes 15.8 us, joined from 60 parts 19.3.  Sequences of up to 512 keys are not
-  // split at all: the join takes as long as the keys that it saves a CTA (12.8 and 12.9 us at 500 keys, 14.6 and 18.4
-  // us at 1000), and a second launch and a workspace.
+  // How the work is cut and shared out (times: Hq32, Hkv8, d128, bf16).  Sequences of up to 512 keys are not split at all: the
+  // join takes as long as the keys that it saves a CTA (B1: 12.8 and 12.9 us at 500 keys, 14.6 and 18.4 us at
+  // 1000), and a second launch and a workspace; every pair has a CTA (B64, 500 keys: 26.9 us, in one wave of CTAs
+  // with two pairs each 29.3).  Longer ones in units of 256 keys, a CTA to each, where those are no more than the
+  // CTAs that run at the same time (B1, 4000 keys: 15.8 us, in units of 64 19.3).  Else that many CTAs share units
+  // of 64 keys evenly.  A pair then counts for as many more units as take the time that a CTA needs to begin
+  // and end with it, 4 to 6 us (B64, 1 to 1000 keys: 51.7 us without, 32.5 with; B64, 1 to 16384: 210 and 191).
   const long long most = 148LL * decode_ctas_per_sm(p.d);
-  const auto units = [&](int log2) {
-    return (long long)B * p.pairs * std::max<long long>(1, ((long long)p.max_len + (1 << log2) - 1) >> log2);
+  const auto units = [&] {
+    const long long keys = std::max<long long>(1, ((long long)p.max_len + (1 << p.unit_log2) - 1) >> p.unit_log2);
+    return (long long)B * p.pairs * (keys + p.unit_extra);
   };
-  p.unit_log2 = p.max_len <= 512 ? 9 : units(8) <= most ? 8 : 6;
-  while (units(p.unit_log2) >= (1LL << 31) && p.unit_log2 < 30) ++p.unit_log2;
-  if (units(p.unit_log2) >= (1LL << 31)) return SAGE_ERR_INVALID_ARG;
-  p.ctas = (uint32_t)std::min<long long>(units(p.unit_log2), most);
+  p.unit_extra = 0, p.unit_log2 = p.max_len <= 512 ? 9 : 8;
+  if (p.unit_log2 == 8 && units() > most) p.unit_extra = p.d <= 64 ? 8 : p.d <= 128 ? 6 : 4, p.unit_log2 = 6;
+  while (units() >= (1LL << 31) && p.unit_log2 < 30) ++p.unit_log2;
+  if (units() >= (1LL << 31)) return SAGE_ERR_INVALID_ARG;
+  const bool split = p.max_len > 1 << p.unit_log2;  // a pair may cross CTAs
+  p.ctas = (uint32_t)(split ? std::min<long long>(units(), most) : units());
   unsigned char* ws = nullptr;
-  if (p.max_len > 1 << p.unit_log2) {  // a pair may cross CTAs
+  if (split) {
     const size_t parts = (size_t)p.ctas * 2 * kDecodeHeads;
     const size_t ml = align_up(parts * 8), total = ml + parts * p.map.dc * 4;
     const cudaError_t e = workspace_alloc(reinterpret_cast<void**>(&ws), total, st);

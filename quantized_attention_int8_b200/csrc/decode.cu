@@ -176,13 +176,16 @@ __device__ __forceinline__ int seq_len_of(const DecodeParams& p, int b, bool rep
   return 0;
 }
 
-// The work, cut into units of 2^unit_log2 keys (the launch says which) of one (sequence, kv head, tile
-// of heads): sequence by sequence, its pairs of kv head and head tile one after the other.  Every CTA takes
-// the same number of units, whatever the sequences' lengths, so that a ragged batch ends everywhere at
-// once; a pair that crosses CTAs is joined.
-__device__ __forceinline__ uint32_t units_of(const DecodeParams& p, int len) {
+// The work, cut into units: 2^unit_log2 keys (the launch says how many) of one (sequence, kv head, tile of heads),
+// sequence by sequence, its pairs of kv head and head tile one after the other.  Every CTA takes the same
+// number of units, whatever the sequences' lengths, so that a ragged batch ends everywhere at once; a
+// pair that crosses CTAs is joined.  Each pair begins with `unit_extra` units without keys, for the time that a CTA
+// needs to begin with it (Q, a full ring) and to write its answer: with keys alone, the CTAs of a ragged
+// batch that got the shortest sequences were its last.
+__device__ __forceinline__ uint32_t key_units(const DecodeParams& p, int len) {
   return len > 0 ? ((uint32_t)(len - 1) >> p.unit_log2) + 1 : 1;  // an empty sequence: one, to write its zeros
 }
+__device__ __forceinline__ uint32_t units_of(const DecodeParams& p, int len) { return key_units(p, len) + p.unit_extra; }
 
 struct Place {
   uint32_t share;     // units per CTA
@@ -274,298 +277,303 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
 
   while (true) {  // one segment: this CTA's keys of one pair
     const uint32_t n_pair = units_of(p, len), rel = unit - pair0, n_seg = min(n_pair - rel, unit_end - unit);
-    const int hkv = pair / p.tiles, head0 = (pair % p.tiles) * kHeads;  // first head within the group
-    const int nheads = min(kHeads, p.G - head0);
-    const int k0 = (int)(rel << p.unit_log2);
-    const int k1 = n_seg == n_pair - rel ? len : (int)((rel + n_seg) << p.unit_log2);
+    // its key units u0 .. u1 - 1 (none where only the pair's first, empty units are this CTA's)
+    const uint32_t u0 = max(rel, p.unit_extra) - p.unit_extra, u1 = max(rel + n_seg, p.unit_extra) - p.unit_extra;
+    if (u0 < u1) {
+      const int hkv = pair / p.tiles, head0 = (pair % p.tiles) * kHeads;  // first head within the group
+      const int nheads = min(kHeads, p.G - head0);
+      const int k0 = (int)(u0 << p.unit_log2);
+      const int k1 = rel + n_seg == n_pair ? len : (int)(u1 << p.unit_log2);
 
-    // ---- this warp's run of 16-key tiles, each of one page (page sizes are multiples of 16)
-    const int ntiles = (k1 - k0 + 15) >> 4, per_warp = (ntiles + kWarps - 1) / kWarps;
-    const int tile0 = min(warp * per_warp, ntiles), n_mine = min(per_warp, ntiles - tile0);
-    const int j0 = k0 + 16 * tile0, j1 = min(k1, j0 + 16 * n_mine);
-    const int steps = (n_mine + R::kTiles - 1) / R::kTiles;
-    // Lanes 8 x .. 8 x + 6 copy tile x of a step: its K rows, four groups of V rows, the scales of each.
-    const int32_t* table = p.map.table + b * p.map.table_stride;
-    const int my_tile = lane >> 3, my_part = lane & 7;
-    const auto my_page = [&](int step) {
-      const int i = step * R::kTiles + my_tile;
-      return my_tile < R::kTiles && i < n_mine ? table[(j0 + 16 * i) >> p.map.page_log2] : -1;
-    };
-    int stage_in = 0, page = my_page(0);
-    uint32_t there = 0;  // bit x: the tile fetched x tiles ago was copied (exists, and not on a bad page)
-    const auto fetch_step = [&](int step) {
-      if (step < steps) {
-        const int i = step * R::kTiles + my_tile, j = j0 + 16 * i;
-        const bool mine = my_tile < R::kTiles && i < n_mine, good = (unsigned)page < (unsigned)p.map.num_pages;
-        if (mine && !good && my_part == 0) atomicOr(&g_decode_error, kBadArg);
-        const uint32_t copied = __ballot_sync(0xffffffffu, mine && good && my_part == 0);
-        const uint32_t bar = bars + 8 * stage_in;
-        if (lane == 0) barrier_expect(bar, __popc(copied) * (32 * dc + 128));
-        __syncwarp();
-        if (mine && good && my_part < 7) {
-          const long long row = p.map.row(page, hkv, j);
-          uint32_t dst = smem_addr(ring) + (stage_in * R::kTiles + my_tile) * tile_bytes, bytes = 16 * dc;
-          const void* src = p.map.k8 + row * dc;
-          if (my_part > 4) {
-            bytes = 64, src = (my_part == 5 ? p.map.ks : p.map.vs) + row, dst += R::scales_at(dc) + (my_part - 5) * 64;
-          } else if (my_part > 0) {
-            bytes = 4 * dc, src = p.map.v8 + (row + 4 * (my_part - 1)) * dc;
-            dst += R::v_at(dc) + (my_part - 1) * R::v_group(dc);
-          }
-          copy_bulk(dst, src, bytes, bar);
-        }
-#pragma unroll
-        for (int x = 0; x < R::kTiles; ++x) there = there << 1 | (copied >> (8 * x) & 1);
-      } else {
-        there <<= R::kTiles;
-      }
-      stage_in = stage_in + 1 == R::kStages ? 0 : stage_in + 1;
-      page = my_page(step + 1);
-    };
-#pragma unroll 1
-    for (int i = 0; i < R::kStages - 1; ++i) fetch_step(i);
-
-    // ---- Q: B operand of S^T.  Step (c, i) of the channels takes from lane t the channels
-    // 64 c + 16 t + 4 i .. + 3 of head g.  As fp16 whatever its type: a bf16 head is scaled by the power of two that
-    // takes its largest value to 2^14 .. 2^15, which is exact down to 2^-29 of that value and rounds to
-    // 2^-40 of it below (fp32 sums are off by more).
-#pragma unroll 1
-    for (int head = warp; head < kHeads; head += kWarps) {
-      const T* q = static_cast<const T*>(p.q.ptr) + (long long)b * p.q.batch +
-                   (long long)(hkv * p.G + head0 + head) * p.q.head;
-      float x[DP / 32];
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < DP / 32; ++e) {
-        const int c = lane + 32 * e;
-        x[e] = head < nheads && c < p.d ? to_f32(q[c]) : 0.f;
-        top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-      }
-      float up = 1.f, hf = p.scale_log2;
-      if (!kSplitP) {
-        top = __reduce_max_sync(0xffffffffu, top);
-        const int e = min(max(127 + 14 - (int)(top >> 23), -126), 126);
-        up = __uint_as_float((uint32_t)(127 + e) << 23), hf *= __uint_as_float((uint32_t)(127 - e) << 23);
-      }
-#pragma unroll
-      for (int e = 0; e < DP / 32; ++e) sm_q[head * QP + lane + 32 * e] = __float2half_rn(x[e] * up);
-      if (lane == 0) sm_hf[head] = hf;
-    }
-    __syncthreads();
-    uint2 qf[KC * 4];
-#pragma unroll
-    for (int s = 0; s < KC * 4; ++s)
-      qf[s] = *reinterpret_cast<const uint2*>(sm_q + g * QP + 64 * (s >> 2) + 16 * t + 4 * (s & 3));
-    const float hf[2] = {sm_hf[2 * t], sm_hf[2 * t + 1]};  // score factor of heads 2t and 2t + 1
-
-    float o[VC * VW * 2][4];  // O^T: tile (q VW + w) 2 + hh holds channels 8 VP q + VP g + 4 w + 2 hh, + 1 (rows g, g + 8) of heads 2t, 2t + 1
-#pragma unroll
-    for (int m = 0; m < VC * VW * 2; ++m)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[m][e] = 0.f;
-    float ms[2] = {-FLT_MAX, -FLT_MAX}, mw[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
-
-    const int krow = (4 * (g >> 1) + (g & 1));  // key of S's row g; two more for row g + 8
-    const unsigned char* const k_lane = ring + krow * dc + 16 * t;
-    const unsigned char* const v_lane = ring + R::v_at(dc) + t * R::v_group(dc) + VP * g;
-    int stage = 0;
-#pragma unroll 1
-    for (int it = 0; it < steps; ++it) {
-      const bool arrived = barrier_wait(bars + 8 * stage, parity >> stage & 1);
-      parity ^= 1u << stage;
-      if (!__all_sync(0xffffffffu, arrived)) {  // gave up: wind down, with the copies in flight given their time
-        for (int x = 1; x < R::kStages - 1 && it + x < steps; ++x) barrier_wait(bars + 8 * ((stage + x) % R::kStages),
-                                                                           parity >> (stage + x) % R::kStages & 1);
-        sm_dead = 1;
-        break;
-      }
-      // (past the vote: all lanes are done with the stage filled next)
-      fetch_step(it + R::kStages - 1);
-      const int at_stage = stage * R::kTiles * tile_bytes;
-      stage = stage + 1 == R::kStages ? 0 : stage + 1;
-
-      // Keys of each tile that count.  V rows behind them (whatever their page holds, or held before) become
-      // zeros: a weight of 0 times a NaN code would be a NaN.
-      int n[R::kTiles];
-#pragma unroll
-      for (int x = 0; x < R::kTiles; ++x) {
-        n[x] = there >> (R::kStages * R::kTiles - 1 - x) & 1 ? min(16, j1 - (j0 + 16 * (it * R::kTiles + x))) : 0;
-        if (n[x] < 16) {
-          unsigned char* v = ring + at_stage + x * tile_bytes + R::v_at(dc);
-#pragma unroll 1
-          for (int r = n[x] + (lane >> 3); r < 16; r += 4)
-#pragma unroll 1
-            for (int c = 16 * (lane & 7); c < dc; c += 128)
-              *reinterpret_cast<uint4*>(v + (r >> 2) * R::v_group(dc) + (r & 3) * dc + c) = make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later copy into the stage
+      // ---- this warp's run of 16-key tiles, each of one page (page sizes are multiples of 16)
+      const int ntiles = (k1 - k0 + 15) >> 4, per_warp = (ntiles + kWarps - 1) / kWarps;
+      const int tile0 = min(warp * per_warp, ntiles), n_mine = min(per_warp, ntiles - tile0);
+      const int j0 = k0 + 16 * tile0, j1 = min(k1, j0 + 16 * n_mine);
+      const int steps = (n_mine + R::kTiles - 1) / R::kTiles;
+      // Lanes 8 x .. 8 x + 6 copy tile x of a step: its K rows, four groups of V rows, the scales of each.
+      const int32_t* table = p.map.table + b * p.map.table_stride;
+      const int my_tile = lane >> 3, my_part = lane & 7;
+      const auto my_page = [&](int step) {
+        const int i = step * R::kTiles + my_tile;
+        return my_tile < R::kTiles && i < n_mine ? table[(j0 + 16 * i) >> p.map.page_log2] : -1;
+      };
+      int stage_in = 0, page = my_page(0);
+      uint32_t there = 0;  // bit x: the tile fetched x tiles ago was copied (exists, and not on a bad page)
+      const auto fetch_step = [&](int step) {
+        if (step < steps) {
+          const int i = step * R::kTiles + my_tile, j = j0 + 16 * i;
+          const bool mine = my_tile < R::kTiles && i < n_mine, good = (unsigned)page < (unsigned)p.map.num_pages;
+          if (mine && !good && my_part == 0) atomicOr(&g_decode_error, kBadArg);
+          const uint32_t copied = __ballot_sync(0xffffffffu, mine && good && my_part == 0);
+          const uint32_t bar = bars + 8 * stage_in;
+          if (lane == 0) barrier_expect(bar, __popc(copied) * (32 * dc + 128));
           __syncwarp();
+          if (mine && good && my_part < 7) {
+            const long long row = p.map.row(page, hkv, j);
+            uint32_t dst = smem_addr(ring) + (stage_in * R::kTiles + my_tile) * tile_bytes, bytes = 16 * dc;
+            const void* src = p.map.k8 + row * dc;
+            if (my_part > 4) {
+              bytes = 64, src = (my_part == 5 ? p.map.ks : p.map.vs) + row, dst += R::scales_at(dc) + (my_part - 5) * 64;
+            } else if (my_part > 0) {
+              bytes = 4 * dc, src = p.map.v8 + (row + 4 * (my_part - 1)) * dc;
+              dst += R::v_at(dc) + (my_part - 1) * R::v_group(dc);
+            }
+            copy_bulk(dst, src, bytes, bar);
+          }
+#pragma unroll
+          for (int x = 0; x < R::kTiles; ++x) there = there << 1 | (copied >> (8 * x) & 1);
+        } else {
+          there <<= R::kTiles;
         }
-      }
+        stage_in = stage_in + 1 == R::kStages ? 0 : stage_in + 1;
+        page = my_page(step + 1);
+      };
+#pragma unroll 1
+      for (int i = 0; i < R::kStages - 1; ++i) fetch_step(i);
 
-      float s[R::kTiles][4], w[R::kTiles][4];  // rows g (0, 1) and g + 8 (2, 3) of heads 2t and 2t + 1
+      // ---- Q: B operand of S^T.  Step (c, i) of the channels takes from lane t the channels
+      // 64 c + 16 t + 4 i .. + 3 of head g.  As fp16 whatever its type: a bf16 head is scaled by the power of two that
+      // takes its largest value to 2^14 .. 2^15, which is exact down to 2^-29 of that value and rounds to
+      // 2^-40 of it below (fp32 sums are off by more).
+#pragma unroll 1
+      for (int head = warp; head < kHeads; head += kWarps) {
+        const T* q = static_cast<const T*>(p.q.ptr) + (long long)b * p.q.batch +
+                     (long long)(hkv * p.G + head0 + head) * p.q.head;
+        float x[DP / 32];
+        uint32_t top = 0;
 #pragma unroll
-      for (int x = 0; x < R::kTiles; ++x)
+        for (int e = 0; e < DP / 32; ++e) {
+          const int c = lane + 32 * e;
+          x[e] = head < nheads && c < p.d ? to_f32(q[c]) : 0.f;
+          top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+        }
+        float up = 1.f, hf = p.scale_log2;
+        if (!kSplitP) {
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int e = min(max(127 + 14 - (int)(top >> 23), -126), 126);
+          up = __uint_as_float((uint32_t)(127 + e) << 23), hf *= __uint_as_float((uint32_t)(127 - e) << 23);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
+        for (int e = 0; e < DP / 32; ++e) sm_q[head * QP + lane + 32 * e] = __float2half_rn(x[e] * up);
+        if (lane == 0) sm_hf[head] = hf;
+      }
+      __syncthreads();
+      uint2 qf[KC * 4];
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        uint4 rows[R::kTiles][2];
+      for (int s = 0; s < KC * 4; ++s)
+        qf[s] = *reinterpret_cast<const uint2*>(sm_q + g * QP + 64 * (s >> 2) + 16 * t + 4 * (s & 3));
+      const float hf[2] = {sm_hf[2 * t], sm_hf[2 * t + 1]};  // score factor of heads 2t and 2t + 1
+
+      float o[VC * VW * 2][4];  // O^T: tile (q VW + w) 2 + hh holds channels 8 VP q + VP g + 4 w + 2 hh, + 1 (rows g, g + 8) of heads 2t, 2t + 1
+#pragma unroll
+      for (int m = 0; m < VC * VW * 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[m][e] = 0.f;
+      float ms[2] = {-FLT_MAX, -FLT_MAX}, mw[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
+
+      const int krow = (4 * (g >> 1) + (g & 1));  // key of S's row g; two more for row g + 8
+      const unsigned char* const k_lane = ring + krow * dc + 16 * t;
+      const unsigned char* const v_lane = ring + R::v_at(dc) + t * R::v_group(dc) + VP * g;
+      int stage = 0;
+#pragma unroll 1
+      for (int it = 0; it < steps; ++it) {
+        const bool arrived = barrier_wait(bars + 8 * stage, parity >> stage & 1);
+        parity ^= 1u << stage;
+        if (!__all_sync(0xffffffffu, arrived)) {  // gave up: wind down, with the copies in flight given their time
+          for (int x = 1; x < R::kStages - 1 && it + x < steps; ++x) barrier_wait(bars + 8 * ((stage + x) % R::kStages),
+                                                                             parity >> (stage + x) % R::kStages & 1);
+          sm_dead = 1;
+          break;
+        }
+        // (past the vote: all lanes are done with the stage filled next)
+        fetch_step(it + R::kStages - 1);
+        const int at_stage = stage * R::kTiles * tile_bytes;
+        stage = stage + 1 == R::kStages ? 0 : stage + 1;
+
+        // Keys of each tile that count.  V rows behind them (whatever their page holds, or held before) become
+        // zeros: a weight of 0 times a NaN code would be a NaN.
+        int n[R::kTiles];
+#pragma unroll
+        for (int x = 0; x < R::kTiles; ++x) {
+          n[x] = there >> (R::kStages * R::kTiles - 1 - x) & 1 ? min(16, j1 - (j0 + 16 * (it * R::kTiles + x))) : 0;
+          if (n[x] < 16) {
+            unsigned char* v = ring + at_stage + x * tile_bytes + R::v_at(dc);
+#pragma unroll 1
+            for (int r = n[x] + (lane >> 3); r < 16; r += 4)
+#pragma unroll 1
+              for (int c = 16 * (lane & 7); c < dc; c += 128)
+                *reinterpret_cast<uint4*>(v + (r >> 2) * R::v_group(dc) + (r & 3) * dc + c) = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later copy into the stage
+            __syncwarp();
+          }
+        }
+
+        float s[R::kTiles][4], w[R::kTiles][4];  // rows g (0, 1) and g + 8 (2, 3) of heads 2t and 2t + 1
 #pragma unroll
         for (int x = 0; x < R::kTiles; ++x)
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            rows[x][r] = *reinterpret_cast<const uint4*>(k_lane + at_stage + x * tile_bytes + 2 * r * dc + 64 * c);
+          for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int c = 0; c < KC; ++c) {
+          uint4 rows[R::kTiles][2];
 #pragma unroll
-          for (int x = 0; x < R::kTiles; ++x) {
-            const uint32_t w0 = (&rows[x][0].x)[i] ^ 0x80808080u, w1 = (&rows[x][1].x)[i] ^ 0x80808080u;
-            mma16816(s[x], widen_int8(w0, 0x4140), widen_int8(w1, 0x4140), widen_int8(w0, 0x4342),
-                     widen_int8(w1, 0x4342), qf[4 * c + i].x, qf[4 * c + i].y);
+          for (int x = 0; x < R::kTiles; ++x)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              rows[x][r] = *reinterpret_cast<const uint4*>(k_lane + at_stage + x * tile_bytes + 2 * r * dc + 64 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int x = 0; x < R::kTiles; ++x) {
+              const uint32_t w0 = (&rows[x][0].x)[i] ^ 0x80808080u, w1 = (&rows[x][1].x)[i] ^ 0x80808080u;
+              mma16816(s[x], widen_int8(w0, 0x4140), widen_int8(w1, 0x4140), widen_int8(w0, 0x4342),
+                       widen_int8(w1, 0x4342), qf[4 * c + i].x, qf[4 * c + i].y);
+            }
+        }
+        bool move = false;
+#pragma unroll
+        for (int x = 0; x < R::kTiles; ++x) {
+          const float* scales = reinterpret_cast<const float*>(ring + at_stage + x * tile_bytes + R::scales_at(dc));
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int key = krow + 2 * r;
+            const float kf = scales[key], lv = lg2(scales[16 + key]);
+            const bool in = key < n[x];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int e = 2 * r + h;
+              s[x][e] = in ? s[x][e] * hf[h] * kf : -INFINITY;
+              w[x][e] = in ? s[x][e] + lv : -INFINITY;
+            }
           }
-      }
-      bool move = false;
 #pragma unroll
-      for (int x = 0; x < R::kTiles; ++x) {
-        const float* scales = reinterpret_cast<const float*>(ring + at_stage + x * tile_bytes + R::scales_at(dc));
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int key = krow + 2 * r;
-          const float kf = scales[key], lv = lg2(scales[16 + key]);
-          const bool in = key < n[x];
+          for (int h = 0; h < 2; ++h)
+            move |= fmaxf(s[x][h], s[x][2 + h]) > ms[h] + kLag || fmaxf(w[x][h], w[x][2 + h]) > mw[h] + kLag;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          float f[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int e = 2 * r + h;
-            s[x][e] = in ? s[x][e] * hf[h] * kf : -INFINITY;
-            w[x][e] = in ? s[x][e] + lv : -INFINITY;
+            float ts = fmaxf(s[0][h], s[0][2 + h]), tw = fmaxf(w[0][h], w[0][2 + h]);
+#pragma unroll
+            for (int x = 1; x < R::kTiles; ++x)
+              ts = fmaxf(ts, fmaxf(s[x][h], s[x][2 + h])), tw = fmaxf(tw, fmaxf(w[x][h], w[x][2 + h]));
+            const float nms = fmaxf(ms[h], max_over_keys(ts)), nmw = fmaxf(mw[h], max_over_keys(tw));
+            l[h] *= ex2(ms[h] - nms);
+            f[h] = ex2(mw[h] - nmw);
+            ms[h] = nms, mw[h] = nmw;
           }
+#pragma unroll
+          for (int m = 0; m < VC * VW * 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[m][e] *= f[e & 1];
         }
+        // P^T as B operand: fp16.  For fp16 outputs a second fp16 term carries what the first rounds off
+        // (2^-12 of a weight would be as large as the output's own rounding).
+        uint32_t ph[R::kTiles][2], pl[R::kTiles][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          move |= fmaxf(s[x][h], s[x][2 + h]) > ms[h] + kLag || fmaxf(w[x][h], w[x][2 + h]) > mw[h] + kLag;
-      }
-      if (__any_sync(0xffffffffu, move)) {
-        float f[2];
+        for (int x = 0; x < R::kTiles; ++x) {
+          float pw[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float ts = fmaxf(s[0][h], s[0][2 + h]), tw = fmaxf(w[0][h], w[0][2 + h]);
-#pragma unroll
-          for (int x = 1; x < R::kTiles; ++x)
-            ts = fmaxf(ts, fmaxf(s[x][h], s[x][2 + h])), tw = fmaxf(tw, fmaxf(w[x][h], w[x][2 + h]));
-          const float nms = fmaxf(ms[h], max_over_keys(ts)), nmw = fmaxf(mw[h], max_over_keys(tw));
-          l[h] *= ex2(ms[h] - nms);
-          f[h] = ex2(mw[h] - nmw);
-          ms[h] = nms, mw[h] = nmw;
-        }
-#pragma unroll
-        for (int m = 0; m < VC * VW * 2; ++m)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[m][e] *= f[e & 1];
-      }
-      // P^T as B operand: fp16.  For fp16 outputs a second fp16 term carries what the first rounds off
-      // (2^-12 of a weight would be as large as the output's own rounding).
-      uint32_t ph[R::kTiles][2], pl[R::kTiles][2];
-#pragma unroll
-      for (int x = 0; x < R::kTiles; ++x) {
-        float pw[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          l[e & 1] += ex2(s[x][e] - ms[e & 1]);
-          pw[e] = ex2(w[x][e] - mw[e & 1]);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const __half2 hi = __floats2half2_rn(pw[2 * r], pw[2 * r + 1]);
-          ph[x][r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
-          if (kSplitP) {
-            const float2 back = __half22float2(hi);
-            const __half2 lo = __floats2half2_rn(pw[2 * r] - back.x, pw[2 * r + 1] - back.y);
-            pl[x][r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
+          for (int e = 0; e < 4; ++e) {
+            l[e & 1] += ex2(s[x][e] - ms[e & 1]);
+            pw[e] = ex2(w[x][e] - mw[e & 1]);
           }
-        }
-      }
 #pragma unroll
-      for (int x = 0; x < R::kTiles; ++x)
-#pragma unroll
-        for (int q = 0; q < VC; ++q) {
-          uint32_t vc[4][VW];  // keys 4 t .. 4 t + 3
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const unsigned char* src = v_lane + at_stage + x * tile_bytes + r * dc + 8 * VP * q;
-            if (VP == 8) {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
-              vc[r][0] = v.x, vc[r][1] = v.y;
-            } else {
-              const uint4 v = *reinterpret_cast<const uint4*>(src);
-              vc[r][0] = v.x, vc[r][1] = v.y, vc[r][VW - 2] = v.z, vc[r][VW - 1] = v.w;
+          for (int r = 0; r < 2; ++r) {
+            const __half2 hi = __floats2half2_rn(pw[2 * r], pw[2 * r + 1]);
+            ph[x][r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
+            if (kSplitP) {
+              const float2 back = __half22float2(hi);
+              const __half2 lo = __floats2half2_rn(pw[2 * r] - back.x, pw[2 * r + 1] - back.y);
+              pl[x][r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
             }
           }
-#pragma unroll
-          for (int wd = 0; wd < VW; ++wd)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t sel = hh ? 0x7362 : 0x5140;
-              const uint32_t x0 = __byte_perm(vc[0][wd], vc[1][wd], sel), x1 = __byte_perm(vc[2][wd], vc[3][wd], sel);
-              const uint32_t a0 = widen_e4m3(x0 & 0xFFFFu), a1 = widen_e4m3(x0 >> 16), a2 = widen_e4m3(x1 & 0xFFFFu),
-                             a3 = widen_e4m3(x1 >> 16);
-              float(&om)[4] = o[(q * VW + wd) * 2 + hh];
-              mma16816(om, a0, a1, a2, a3, ph[x][0], ph[x][1]);
-              if (kSplitP) mma16816(om, a0, a1, a2, a3, pl[x][0], pl[x][1]);
-            }
         }
-    }
+#pragma unroll
+        for (int x = 0; x < R::kTiles; ++x)
+#pragma unroll
+          for (int q = 0; q < VC; ++q) {
+            uint32_t vc[4][VW];  // keys 4 t .. 4 t + 3
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const unsigned char* src = v_lane + at_stage + x * tile_bytes + r * dc + 8 * VP * q;
+              if (VP == 8) {
+                const uint2 v = *reinterpret_cast<const uint2*>(src);
+                vc[r][0] = v.x, vc[r][1] = v.y;
+              } else {
+                const uint4 v = *reinterpret_cast<const uint4*>(src);
+                vc[r][0] = v.x, vc[r][1] = v.y, vc[r][VW - 2] = v.z, vc[r][VW - 1] = v.w;
+              }
+            }
+#pragma unroll
+            for (int wd = 0; wd < VW; ++wd)
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const uint32_t sel = hh ? 0x7362 : 0x5140;
+                const uint32_t x0 = __byte_perm(vc[0][wd], vc[1][wd], sel), x1 = __byte_perm(vc[2][wd], vc[3][wd], sel);
+                const uint32_t a0 = widen_e4m3(x0 & 0xFFFFu), a1 = widen_e4m3(x0 >> 16), a2 = widen_e4m3(x1 & 0xFFFFu),
+                               a3 = widen_e4m3(x1 >> 16);
+                float(&om)[4] = o[(q * VW + wd) * 2 + hh];
+                mma16816(om, a0, a1, a2, a3, ph[x][0], ph[x][1]);
+                if (kSplitP) mma16816(om, a0, a1, a2, a3, pl[x][0], pl[x][1]);
+              }
+          }
+      }
 
-    // ---- join the warps: O moves to the reference of the scores, then to the largest one
+      // ---- join the warps: O moves to the reference of the scores, then to the largest one
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
-      if (g == 0) sm_m[warp][2 * t + h] = ms[h], sm_l[warp][2 * t + h] = l[h];
-    }
-    __syncthreads();  // and every warp is done with its ring
-    float* const sm_o = reinterpret_cast<float*>(smem);
+        for (int x = 4; x < 32; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+        if (g == 0) sm_m[warp][2 * t + h] = ms[h], sm_l[warp][2 * t + h] = l[h];
+      }
+      __syncthreads();  // and every warp is done with its ring
+      float* const sm_o = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int head = 2 * t + h;
-      float top = sm_m[0][head];
+      for (int h = 0; h < 2; ++h) {
+        const int head = 2 * t + h;
+        float top = sm_m[0][head];
 #pragma unroll
-      for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm_m[x][head]);
-      const float f = ex2(mw[h] - top);
+        for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm_m[x][head]);
+        const float f = ex2(mw[h] - top);
 #pragma unroll
-      for (int q = 0; q < VC; ++q)
+        for (int q = 0; q < VC; ++q)
 #pragma unroll
-        for (int m = 0; m < VW * 2; ++m) {
-          float* dst = sm_o + (warp * kHeads + head) * DP + 8 * VP * q + VP * g + 2 * m;
-          *reinterpret_cast<float2*>(dst) = make_float2(o[q * VW * 2 + m][h] * f, o[q * VW * 2 + m][2 + h] * f);
-        }
-    }
-    __syncthreads();
-    const bool whole = n_seg == n_pair;  // this CTA saw all of the pair's keys
-    const int part = blockIdx.x * 2 + (rel > 0 ? 0 : 1);  // a CTA's first pair may have begun before it, its last go on
+          for (int m = 0; m < VW * 2; ++m) {
+            float* dst = sm_o + (warp * kHeads + head) * DP + 8 * VP * q + VP * g + 2 * m;
+            *reinterpret_cast<float2*>(dst) = make_float2(o[q * VW * 2 + m][h] * f, o[q * VW * 2 + m][2 + h] * f);
+          }
+      }
+      __syncthreads();
+      const bool whole = u0 == 0 && rel + n_seg == n_pair;  // this CTA saw all of the pair's keys
+      const int part = blockIdx.x * 2 + (u0 > 0 ? 0 : 1);  // a CTA's first pair may have begun before it, its last go on
 #pragma unroll 1
-    for (int i = threadIdx.x; i < nheads * DP; i += kThreads) {
-      const int head = i / DP, c = i % DP;
-      if (c >= p.d) continue;
-      float top = sm_m[0][head], sum = 0.f, acc = 0.f;
+      for (int i = threadIdx.x; i < nheads * DP; i += kThreads) {
+        const int head = i / DP, c = i % DP;
+        if (c >= p.d) continue;
+        float top = sm_m[0][head], sum = 0.f, acc = 0.f;
 #pragma unroll
-      for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm_m[x][head]);
+        for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm_m[x][head]);
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x)
-        sum += sm_l[x][head] * ex2(sm_m[x][head] - top), acc += sm_o[(x * kHeads + head) * DP + c];
-      if (whole) {
-        T* dst = static_cast<T*>(p.out) + ((long long)b * p.Hq + hkv * p.G + head0 + head) * p.d + c;
-        if (SAGE_STORE_OK(p.x_out, dst, 2, &g_decode_error)) *dst = from_f32<T>(sum == 0.f ? 0.f : acc / sum);
-      } else {
-        float* dst = p.part_o + (long long)(part * kHeads + head) * dc + c;
-        if (SAGE_STORE_OK(p.x_part_o, dst, 4, &g_decode_error)) *dst = acc;
-        if (c == 0) {
-          float* ml = p.part_ml + (part * kHeads + head) * 2;
-          if (SAGE_STORE_OK(p.x_part_ml, ml, 8, &g_decode_error)) ml[0] = top, ml[1] = sum;
+        for (int x = 0; x < kWarps; ++x)
+          sum += sm_l[x][head] * ex2(sm_m[x][head] - top), acc += sm_o[(x * kHeads + head) * DP + c];
+        if (whole) {
+          T* dst = static_cast<T*>(p.out) + ((long long)b * p.Hq + hkv * p.G + head0 + head) * p.d + c;
+          if (SAGE_STORE_OK(p.x_out, dst, 2, &g_decode_error)) *dst = from_f32<T>(sum == 0.f ? 0.f : acc / sum);
+        } else {
+          float* dst = p.part_o + (long long)(part * kHeads + head) * dc + c;
+          if (SAGE_STORE_OK(p.x_part_o, dst, 4, &g_decode_error)) *dst = acc;
+          if (c == 0) {
+            float* ml = p.part_ml + (part * kHeads + head) * 2;
+            if (SAGE_STORE_OK(p.x_part_ml, ml, 8, &g_decode_error)) ml[0] = top, ml[1] = sum;
+          }
         }
       }
+      if (sm_dead) return;
     }
     unit += n_seg, pair0 += n_pair;
-    if (unit >= unit_end || sm_dead) return;
+    if (unit >= unit_end) return;
     if (++pair == p.pairs) pair = 0, ++b, len = seq_len_of(p, b, !p.part_o && threadIdx.x == 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();  // O is read: the rings may be filled again
@@ -583,8 +591,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(DecodePara
   __shared__ float4 sm_o[kJoinWarps][32 * V];
   const Place at = find_place<kJoinWarps * 32>(p, blockIdx.x + 1, false);
   if (at.b < 0) return;
-  const uint32_t u = (blockIdx.x + 1) * at.share;
-  if (at.pair0 == u || at.pair0 < u - at.share) return;  // no pair crosses here, or it crossed an earlier border
+  const uint32_t u = (blockIdx.x + 1) * at.share, keys0 = at.pair0 + p.unit_extra;
+  if (u <= keys0 || u - at.share > keys0) return;  // no pair's keys cross here, or they crossed an earlier border
   const int c0 = blockIdx.x, n = (int)((at.pair0 + units_of(p, at.len) - 1) / at.share) - c0 + 1;
   const int hkv = at.pair / p.tiles, head0 = (at.pair % p.tiles) * kHeads, nheads = min(kHeads, p.G - head0);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dc = p.map.dc;

@@ -231,6 +231,7 @@ struct DecodeParams {
   int tiles;       // tiles of 8 query heads per kv head
   uint32_t pairs;  // kv heads x tiles
   int unit_log2;   // keys per unit of work
+  uint32_t unit_extra;  // units without keys that each pair begins with
   uint32_t ctas;   // CTAs that share the work evenly
   float scale_log2;
   float* part_o;   // [2 ctas][8][dc]: a CTA's part of the pair that it begins in, and of the one it ends in (or nullptr)
