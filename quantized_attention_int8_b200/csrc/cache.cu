@@ -516,8 +516,10 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
   }
 }
 
-// Large calls: every CTA takes its share of each kind, one after the other, so that all end together
-// whatever a kind's rows cost.  Small ones (`apart`): the kinds have CTAs of their own, which work at the same time.
+// `apart`: the kinds have CTAs of their own, which work at the same time (a decode step, a chunk of a prompt; norm and
+// rotation alone, whose rows cost the same: video-DiT 138 -> 134 us).  Large cache writes: every CTA takes
+// its share of each kind, one after the other, so that all end together whatever a kind's rows cost (four
+// 8192-token prompts 160 us, apart 209).
 template <typename T, int LPR, int HC, int MODE, bool APPEND>
 __global__ void __launch_bounds__(kThreads, HC > 1 ? 6 : 8) head_rows_kernel(const __grid_constant__ HeadRowsParams p) {
   __shared__ float partner_buf[MODE == kScalar ? kThreads * 8 : 1];
@@ -623,14 +625,22 @@ cudaError_t launch_rows(HeadRowsParams p, cudaStream_t st) {
   constexpr long long kGroups = kThreads / LPR;
   const unsigned most = 148 * (HC > 1 ? 6 : 8);  // one wave
   const auto rounds_of = [&](const HeadRows& k) { return (unsigned)((p.tokens + kGroups - 1) / kGroups * k.chunks); };
-  unsigned all = 0;
   const auto heads = [&](const HeadRows& k) { return heads_at_a_time(HC, p.append, (int)(&k - p.kind)); };
-  for (HeadRows& k : p.kind) k.chunks = (k.H + heads(k) - 1) / heads(k), all += rounds_of(k);
-  p.apart = all <= most;
+  unsigned all = 0;
+  double cost = 0;
+  // a round's time: coded keys 1.45 and values 1.1 times queries' per row (bf16, d 128, norm and rotation)
+  const double weight[3] = {1.0, p.append ? 1.45 * heads_at_a_time(HC, true, kK) / HC : 1.0, 1.1};
+  for (HeadRows& k : p.kind) {
+    k.chunks = (k.H + heads(k) - 1) / heads(k), all += rounds_of(k);
+    cost += rounds_of(k) * weight[&k - p.kind];
+  }
+  p.apart = !p.append || all <= 8 * most;
   unsigned grid = 0;
   for (HeadRows& k : p.kind) {
     const unsigned rounds = rounds_of(k);
-    k.ctas = p.apart ? rounds : most;
+    k.ctas = all <= most ? rounds
+             : p.apart   ? std::min(rounds, std::max(1u, (unsigned)(most * (rounds * weight[&k - p.kind] / cost))))
+                         : most;
     grid = p.apart ? grid + k.ctas : most;
     if (!rounds) continue;
     k.rounds = rounds / k.ctas, k.rounds_more = rounds % k.ctas;

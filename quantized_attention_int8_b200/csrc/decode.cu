@@ -285,6 +285,18 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
       const int k0 = (int)(u0 << p.unit_log2);
       const int k1 = rel + n_seg == n_pair ? len : (int)(u1 << p.unit_log2);
 
+      // Q is asked for before the ring is filled: behind its 15 MB in flight it would come two microseconds later.
+      T qx[kHeads / kWarps][DP / 32];
+#pragma unroll
+      for (int i = 0; i < kHeads / kWarps; ++i) {
+        const int head = warp + i * kWarps;
+        const T* q = static_cast<const T*>(p.q.ptr) + (long long)b * p.q.batch +
+                     (long long)(hkv * p.G + head0 + head) * p.q.head;
+#pragma unroll
+        for (int e = 0; e < DP / 32; ++e)
+          qx[i][e] = head < nheads && lane + 32 * e < p.d ? q[lane + 32 * e] : from_f32<T>(0.f);
+      }
+
       // ---- this warp's run of 16-key tiles, each of one page (page sizes are multiples of 16)
       const int ntiles = (k1 - k0 + 15) >> 4, per_warp = (ntiles + kWarps - 1) / kWarps;
       const int tile0 = min(warp * per_warp, ntiles), n_mine = min(per_warp, ntiles - tile0);
@@ -335,18 +347,14 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
       // 64 c + 16 t + 4 i .. + 3 of head g.  As fp16 whatever its type: a bf16 head is scaled by the power of two that
       // takes its largest value to 2^14 .. 2^15, which is exact down to 2^-29 of that value and rounds to
       // 2^-40 of it below (fp32 sums are off by more).
-#pragma unroll 1
-      for (int head = warp; head < kHeads; head += kWarps) {
-        const T* q = static_cast<const T*>(p.q.ptr) + (long long)b * p.q.batch +
-                     (long long)(hkv * p.G + head0 + head) * p.q.head;
+#pragma unroll
+      for (int i = 0; i < kHeads / kWarps; ++i) {
+        const int head = warp + i * kWarps;
         float x[DP / 32];
         uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < DP / 32; ++e) {
-          const int c = lane + 32 * e;
-          x[e] = head < nheads && c < p.d ? to_f32(q[c]) : 0.f;
-          top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-        }
+        for (int e = 0; e < DP / 32; ++e)
+          x[e] = to_f32(qx[i][e]), top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
         float up = 1.f, hf = p.scale_log2;
         if (!kSplitP) {
           top = __reduce_max_sync(0xffffffffu, top);
@@ -585,9 +593,10 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
 // that is the first border inside it.  Launched as a programmatic dependent: it finds its pair while the
 // other kernel still runs.  Warps share out the tile's heads, then the parts; a warp's loads are in
 // flight eight at a time (one at a time cost 20 us for the 56 parts of a 131072-key sequence).
-constexpr int kJoinWarps = 16, kJoinBatch = 8;
+constexpr int kJoinWarps = 8, kJoinBatch = 8;
 template <typename T, int V>  // V float4 per lane: d <= 128 V
-__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(DecodeParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) decode_join_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int kBatch = kJoinBatch / V;
   __shared__ float4 sm_o[kJoinWarps][32 * V];
   const Place at = find_place<kJoinWarps * 32>(p, blockIdx.x + 1, false);
   if (at.b < 0) return;
@@ -603,34 +612,37 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(DecodePara
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   float top = -FLT_MAX, sum = 0.f;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[part(i)].x);
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(ml + part(i)).x);
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
   float4 acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += kJoinBatch * ways) {
-    float4 o[kJoinBatch][V];
-    float f[kJoinBatch];
+  for (int i0 = way; i0 < n; i0 += kBatch * ways) {
+    // loads without a condition (the last part again behind the last; column 0 behind dc), so that all are in flight
+    float2 x[kBatch];
+    float4 o[kBatch][V];
 #pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k) {
-      const int i = i0 + k * ways + way;
-      const float2 x = i < n ? ml[part(i)] : make_float2(-INFINITY, 0.f);
-      f[k] = ex2(x.x - top);
-      sum += x.y * f[k];
+    for (int k = 0; k < kBatch; ++k) {
+      const long long at_i = part(min(i0 + k * ways, n - 1));
+      x[k] = __ldcg(ml + at_i);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        o[k][v] = i < n && 4 * (lane + 32 * v) < dc
-                      ? *reinterpret_cast<const float4*>(p.part_o + part(i) * dc + 4 * (lane + 32 * v))
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int v = 0; v < V; ++v) {
+        const int c = 4 * (lane + 32 * v);
+        o[k][v] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at_i * dc + (c < dc ? c : 0)));
+      }
     }
 #pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k)
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + k * ways < n) {
+        const float f = ex2(x[k].x - top);
+        sum += x[k].y * f;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        acc[v].x += o[k][v].x * f[k], acc[v].y += o[k][v].y * f[k], acc[v].z += o[k][v].z * f[k],
-            acc[v].w += o[k][v].w * f[k];
+        for (int v = 0; v < V; ++v)
+          acc[v].x += o[k][v].x * f, acc[v].y += o[k][v].y * f, acc[v].z += o[k][v].z * f, acc[v].w += o[k][v].w * f;
+      }
+    }
   }
   __shared__ float sm_l[kJoinWarps];
 #pragma unroll
