@@ -246,11 +246,14 @@ Extent extent_of(const void* ptr, size_t bytes) {
 
 std::atomic<long long> g_out_limit{0};  // test hook: narrows the output extent when > 0
 
-Extent out_extent(const Dims& m, const void* out) {
-  size_t bytes = (size_t)m.total_q * m.Hq * m.d * 2;  // fp16 / bf16 output
+Extent limited_extent(const void* out, size_t bytes) {
   const long long lim = g_out_limit.load();
   if (lim > 0 && (size_t)lim < bytes) bytes = (size_t)lim;
   return extent_of(out, bytes);
+}
+
+Extent out_extent(const Dims& m, const void* out) {
+  return limited_extent(out, (size_t)m.total_q * m.Hq * m.d * 2);  // fp16 / bf16 output
 }
 
 struct QuantBufs {
@@ -858,7 +861,7 @@ sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long 
   const long long room = (long long)max_pages << p.map.page_log2;
   p.max_len = (int)std::min<long long>(std::min<long long>(max_seqlen, room), 1 << 30);
   p.scale_log2 = resolve_scale(sm_scale, p.d) * 1.4426950408889634f;
-  p.x_out = extent_of(out, out_bytes);
+  p.x_out = limited_extent(out, out_bytes);
   if ((s = check_device()) != SAGE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // How the work is cut and shared out (times: Hq32, Hkv8, d128, bf16).  Sequences of up to 512 keys are not split at all: the

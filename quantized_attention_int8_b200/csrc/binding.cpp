@@ -45,6 +45,11 @@ double float_of(PyObject* o) {
   if (v == -1.0 && PyErr_Occurred()) throw BadArgument();
   return v;
 }
+bool bool_of(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw BadArgument();
+  return v == 1;
+}
 int int32_of(PyObject* o, const char* name) {
   const long long v = int_of(o);
   if (v < INT32_MIN || v > INT32_MAX) bad("%s does not fit 32 bits", name);
@@ -103,6 +108,8 @@ Tensor output(PyObject* o, const char* name, const Tensor& like) {
   const Tensor& t = tensor_of(o, name);
   if (!t.sizes().equals(like.sizes())) bad("%s has the wrong shape", name);
   check_heads(t, name, &like);
+  for (int64_t i = 0; i < t.dim(); ++i)
+    if (t.stride(i) == 0 && t.size(i) > 1) bad("%s has elements that share memory", name);
   return t;
 }
 
@@ -140,7 +147,7 @@ const float* k_mean_of(PyObject* o, int64_t Hkv, int64_t d, int dev) {
 sage_norm_rope norm_rope_of(PyObject* const* a, int64_t d, int dev) {
   sage_norm_rope nr = {};
   const Tensor *cs = optional_of(a[0], "cos_sin"), *qw = optional_of(a[1], "q_weight"), *kw = optional_of(a[2], "k_weight");
-  nr.norm = PyObject_IsTrue(a[3]) == 1, nr.eps = (float)float_of(a[4]), nr.interleaved = PyObject_IsTrue(a[5]) == 1;
+  nr.norm = bool_of(a[3]), nr.eps = (float)float_of(a[4]), nr.interleaved = bool_of(a[5]);
   nr.weight_dtype = SAGE_FP32;
   if ((qw || kw) && !nr.norm) bad("q_weight and k_weight need norm=True");
   for (const Tensor* w : {qw, kw})
@@ -156,6 +163,7 @@ sage_norm_rope norm_rope_of(PyObject* const* a, int64_t d, int dev) {
   if (cs) {
     if (cs->scalar_type() != at::kFloat || !cs->is_cuda() || cs->get_device() != dev || cs->dim() != 2 || !cs->is_contiguous())
       bad("cos_sin must be a contiguous float32 tensor (positions, rotary_dim) on the device of the others");
+    if (cs->numel() == 0) bad("cos_sin must not be empty");
     nr.cos_sin = static_cast<const float*>(pointer(cs));
     nr.n_pos = narrow(cs->size(0), "cos_sin"), nr.rot = narrow(cs->size(1), "cos_sin");
   }
@@ -218,7 +226,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& q = tensor_of(a[1], "q");
   const Tensor *k = optional_of(a[2], "k"), *positions = optional_of(a[3], "positions");
   check_heads(q, "q");
-  const bool hnd = PyObject_IsTrue(a[4]) == 1;
+  const bool hnd = bool_of(a[4]);
   const Extents e = extents(q, hnd);
   const int64_t d = q.size(-1);
   const int dev = q.get_device();

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
       const int k0 = (int)(u0 << p.unit_log2);
       const int k1 = rel + n_seg == n_pair ? len : (int)(u1 << p.unit_log2);
 
-      // Q is asked for before the ring is filled: behind its 15 MB in flight it would come two microseconds later.
+      // Q is asked for before the ring is filled, not behind its copies (B64, 1 to 1000 keys: 32.2 -> 30.2 us).
       T qx[kHeads / kWarps][DP / 32];
 #pragma unroll
       for (int i = 0; i < kHeads / kWarps; ++i) {

@@ -340,7 +340,11 @@ DECODE = [  # d, Hq, Hkv, page, lengths, dtype
     (256, 4, 2, 1024, [1025, 90], BF16),
     (64, 64, 2, 16, [33], BF16),            # four tiles
     (128, 32, 8, 64, [2049, 5000, 1], F16),  # split and joined, next to short ones
-    (37, 5, 5, 16, [90, 16], F16),          # scalar loads of q
+    (37, 5, 5, 16, [90, 16], F16),          # an odd head size
+    (64, 16, 16, 16, [1, 500, 0, 300] * 10, F16),           # more pairs than CTAs run at a time, none split
+    (128, 16, 16, 64, [700, 1, 0, 1500, 513, 64] * 6, BF16),  # shares of several short sequences
+    (256, 8, 8, 16, [900, 3, 0, 2000] * 4, F16),
+    (48, 6, 3, 32, [3000, 700], BF16),      # a CTA to each unit
 ]
 
 
@@ -670,6 +674,9 @@ def test_python_layer_refuses(lib):
         lambda: lib.sage_cache_gather(cache, table, lens, 4, 64), lambda: lib.sage_cache_gather(cache, table, cu, 4, 96),
         lambda: lib.sage_attn_decode(x[None], cache, table, lens, 4), lambda: lib.sage_attn_decode(x, cache, table[:1], lens, 4),
         lambda: lib.sage_attn_decode(x, cache, table, lens, 4, out=x.transpose(0, 1)),
+        lambda: lib.sage_qk_norm_rope(x, None, q_out=x[:, :1].expand(2, 4, 64)),  # an output that overlaps itself
+        lambda: lib.sage_qk_norm_rope(x, None, None, cs[:0]), lambda: lib.sage_attn_decode(x, cache, table, lens, 1 << 40),
+        lambda: lib.sage_attn_decode(None, cache, table, lens, 4), lambda: lib.sage_cache_gather(cache, table, cu, -1, 64),
     ]
     accepted = []
     for i, f in enumerate(bad):
@@ -691,6 +698,27 @@ def test_python_layer_refuses(lib):
         lib.sage_qk_norm_rope(x, x, lens, torch.zeros((8, 66), device="cuda"))
     with pytest.raises(lib.SageError):
         lib.sage_attn_decode(x, lib.sage_kv_cache(4, 4, 64, 48), table, lens, 4)
+
+
+def test_narrowed_output_skips_and_reports_decode_stores(lib):
+    # the extent ends inside the second sequence's output: its bytes stay, the first ones are the normal result
+    checked = lib.load_checked()
+    lens = [600, 700]
+    _, table, cache, ld = _decode_setup(lib, lens, 2, 64, 16)
+    q = S.heads((2, 4, 64), F16, 1).cuda()
+    want = lib.sage_attn_decode(q, cache, table, ld, 700)
+    lib.sage_check_status()
+    out, limit = torch.full_like(q, 7.0), 4 * 64 * 2 + 100
+    saved, lib.capi = lib.capi, checked
+    checked.sage_test_out_limit(limit)
+    try:
+        lib.sage_attn_decode(q, cache, table, ld, 700, out=out)
+        assert checked.sage_check_status(torch.cuda.current_stream().cuda_stream) == lib.SAGE_ERR_BOUNDS
+    finally:
+        checked.sage_test_out_limit(0)
+        lib.capi = saved
+    assert torch.equal(S.bits(out)[:limit], S.bits(want)[:limit])
+    assert torch.equal(S.bits(out)[limit:], S.bits(torch.full_like(q, 7.0))[limit:])
 
 
 def test_checked_build_serving_matches(lib):
