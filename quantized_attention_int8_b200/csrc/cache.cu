@@ -43,6 +43,12 @@ constexpr int kBadArg = 2;  // the error word's bit for SAGE_ERR_INVALID_ARG
 // 448 / amax then stay finite.
 constexpr float kTinyAmax = 7.888609052210118e-31f;  // 2^-100
 
+// Lets the next grid be set up (it waits for this one before it touches memory), and waits for the one before.
+__device__ __forceinline__ void begin_dependent() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
@@ -523,6 +529,7 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
 template <typename T, int LPR, int HC, int MODE, bool APPEND>
 __global__ void __launch_bounds__(kThreads, HC > 1 ? 6 : 8) head_rows_kernel(const __grid_constant__ HeadRowsParams p) {
   __shared__ float partner_buf[MODE == kScalar ? kThreads * 8 : 1];
+  begin_dependent();
   const unsigned cta = blockIdx.x, q = p.apart ? p.kind[kQ].ctas : 0, k = p.apart ? q + p.kind[kK].ctas : 0;
   if (!p.apart || cta < q) head_rows<T, LPR, HC, MODE, APPEND, kQ>(p, p.kind[kQ], cta, partner_buf);
   if (!p.apart || (cta >= q && cta < k)) head_rows<T, LPR, heads_at_a_time(HC, APPEND, kK), MODE, APPEND, kK>(p, p.kind[kK], cta - q, partner_buf);
@@ -537,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, HC > 1 ? 6 : 8) head_rows_kernel(con
 template <typename T, int LPR, int HC, bool VEC>
 __global__ void __launch_bounds__(kThreads, HC > 1 ? 5 : 8) gather_kernel(const __grid_constant__ GatherParams p) {
   constexpr unsigned kGroups = kThreads / LPR;
+  begin_dependent();
   const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR, c = lane * 8;
   const unsigned rounds = p.rounds + (blockIdx.x < p.rounds_more ? 1 : 0);
   const unsigned round0 = blockIdx.x * p.rounds + min(blockIdx.x, p.rounds_more);
@@ -651,11 +659,8 @@ cudaError_t launch_rows(HeadRowsParams p, cudaStream_t st) {
     moves(k.in, &k.in_chunk, &k.in_tokens);
     moves(k.out, &k.out_chunk, &k.out_tokens);
   }
-  if (p.append)
-    head_rows_kernel<T, LPR, HC, MODE, true><<<grid, kThreads, 0, st>>>(p);
-  else
-    head_rows_kernel<T, LPR, HC, MODE, false><<<grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return p.append ? launch_dependent(head_rows_kernel<T, LPR, HC, MODE, true>, grid, kThreads, 0, st, p)
+                  : launch_dependent(head_rows_kernel<T, LPR, HC, MODE, false>, grid, kThreads, 0, st, p);
 }
 
 template <typename T, int LPR>
@@ -679,8 +684,7 @@ cudaError_t launch_gather(GatherParams p, cudaStream_t st) {
   const long long rounds = (p.T + kGroups - 1) / kGroups * p.chunks;
   const unsigned grid = (unsigned)std::min<long long>(rounds, 148 * (HC > 1 ? 5 : 8));  // one wave
   p.rounds = (unsigned)(rounds / grid), p.rounds_more = (unsigned)(rounds % grid);
-  gather_kernel<T, LPR, HC, VEC><<<grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(gather_kernel<T, LPR, HC, VEC>, grid, kThreads, 0, st, p);
 }
 
 template <typename T, int LPR>

@@ -268,7 +268,10 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
   if (threadIdx.x == 0) sm_dead = 0;
   if (lane < R::kStages) barrier_init(bars + 8 * lane);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join takes the SMs that this grid frees
+  // The grid before may have written the cache, Q or the lengths.  Only then is the join let in, which reads the
+  // lengths before it waits for this grid; it takes the SMs that this grid frees.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Place at = find_place<kThreads>(p, blockIdx.x, blockIdx.x == 0);
   if (at.b < 0) return;
   uint32_t unit = blockIdx.x * at.share, pair0 = at.pair0, parity = 0;  // parity: bit per stage
@@ -675,19 +678,7 @@ cudaError_t launch_decode_dp(const DecodeParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
-  kernel<<<p.ctas, kThreads, Ring<DP>::cta_bytes(p.map.dc), st>>>(p);
-  return cudaGetLastError();
-}
-
-template <typename T, int V>
-cudaError_t launch_join(const DecodeParams& p, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(p.ctas - 1), cfg.blockDim = dim3(kJoinWarps * 32), cfg.stream = st;
-  cfg.attrs = &attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, V>, p);
+  return launch_dependent(kernel, p.ctas, kThreads, Ring<DP>::cta_bytes(p.map.dc), st, p);
 }
 
 template <typename T>
@@ -696,7 +687,8 @@ cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t st) {
                         : p.d <= 128 ? launch_decode_dp<T, 128>(p, st)
                                      : launch_decode_dp<T, 256>(p, st);
   if (e != cudaSuccess || !p.part_o) return e;
-  return p.d <= 128 ? launch_join<T, 1>(p, st) : launch_join<T, 2>(p, st);
+  return launch_dependent(p.d <= 128 ? decode_join_kernel<T, 1> : decode_join_kernel<T, 2>, p.ctas - 1, kJoinWarps * 32,
+                          0, st, p);
 }
 
 }  // namespace

@@ -239,6 +239,20 @@ struct DecodeParams {
   Extent x_out, x_part_o, x_part_ml;
 };
 
+// Launches a kernel as a programmatic dependent of the one before it in the stream: its CTAs may be set up while
+// that one ends.  The kernel calls griddepcontrol.wait before it touches memory.
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_quantize(const QuantParams& p, cudaStream_t st);
 cudaError_t launch_head_rows(const HeadRowsParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_cache_gather(const GatherParams& p, int dtype, cudaStream_t st);

@@ -577,6 +577,56 @@ def test_decode_step_captured_and_replayed(lib):
     lib.sage_check_status()
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_see_what_the_work_just_before_them_wrote(lib, captured):
+    """The kernels are set up while the work before them ends: lengths, queries and cache rows that it writes (a copy, a
+    torch kernel, an append) are seen all the same.  Two states in turn, many times."""
+    Hq, Hkv, d, ps = 8, 2, 128, 64
+    lens = [[3000, 40, 700, 0], [200, 2900, 1, 1500]]
+    table, pages = S.page_table([3000, 2900, 700, 1500], ps, 0)
+    td = table.cuda()
+    seqs = S.random_sequences([3000, 2900, 700, 1500], Hkv, d, 1)
+    cache = S.poison(lib, pages, Hkv, d, ps)
+    S.fill(cache, table, [3000, 2900, 700, 1500], *seqs, d)
+    ld = [torch.tensor(x, dtype=torch.int32).cuda() for x in lens]
+    rows = [S.heads((4, Hq + 2 * Hkv, d), F16, i).cuda() for i in range(2)]
+    cu = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32).cuda()
+    lens_now, rows_now, out = torch.empty_like(ld[0]), torch.empty_like(rows[0]), torch.empty((4, Hq, d), dtype=F16,
+                                                                                             device="cuda")
+    ko, vo = (torch.empty((4, Hkv, d), dtype=F16, device="cuda") for _ in range(2))
+
+    def step(i):
+        lens_now.copy_(ld[i])
+        torch.mul(rows[i], 1.0, out=rows_now)
+        q = lib.sage_cache_append(cache, rows_now[:, Hq:Hq + Hkv], rows_now[:, Hq + Hkv:], td, lens_now, q=rows_now[:, :Hq],
+                                  norm=True)
+        lib.sage_attn_decode(q, cache, td, lens_now, 3000, out=out)
+        torch.sub(lens_now, 1, out=lens_now)
+        lib.sage_cache_gather(cache, td, cu, 4, d, starts=lens_now.clamp(min=0), k_out=ko, v_out=vo)
+
+    runs = [lambda i=i: step(i) for i in range(2)]
+    want = []
+    for i in (0, 1, 0, 1):  # (the appended rows settle in the first round)
+        step(i)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (out, ko, vo)])
+    if captured:
+        graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+        for i, g in enumerate(graphs):
+            with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+                step(i)
+        runs = [g.replay for g in graphs]
+    got = []
+    for _ in range(100):
+        for i in range(2):
+            runs[i]()
+            got.append([t.clone() for t in (out, ko, vo)])
+    lib.sage_check_status()
+    for n, ts in enumerate(got):
+        for a, b in zip(ts, want[2 + n % 2]):
+            assert torch.equal(S.bits(a), S.bits(b)), n
+
+
 # ------------------------------------------------------------------------------------------ together
 @pytest.mark.parametrize("dt,mean", [(F16, False), (BF16, True)])
 def test_prompt_chunk_and_steps_together(lib, dt, mean):
