@@ -10,7 +10,14 @@
 // cache write with norm and rotation the key goes from fp32 straight to its INT8 code: rounding it
 // to 16 bits in between would only add error.
 //
-// Everything here moves bytes: about ten operations per element.  A row (one head of one token) is
+// Everything here moves bytes: about ten operations per element.  Norm and rotation of the video-DiT heads (B1
+// N32768 Hq24 Hkv24 d128 bf16, 822 MB) take 134 us, 6.1 TB/s: HBM bounds them.  The write of four
+// 8192-token prompts (Hq32 Hkv8 d128 fp16 with norm, rotation and k_mean, 740 MB) takes 160 us, 4.6
+// TB/s: the coded rows (two thirds of the instructions, a third of the rows) are bound by instruction issue and the
+// latency between their two reductions.  The read back of 16 prefixes (1 to 8192 tokens, Hkv8 d128, 401 MB) takes
+// 75 us, 5.3 TB/s: the loads' latency, at 20 warps to an SM.  Short calls are launch latency: 4 to 5 us.
+//
+// A row (one head of one token) is
 // owned by 8, 16 or 32 consecutive lanes, eight channels to a lane, so that the sum of squares and
 // the amax are lane shuffles and no barrier is on the path.  Where halves rotate together a lane owns
 // four channels of each half, at the same place: both partners of its four pairs, and four angles
@@ -281,10 +288,9 @@ enum RowKind { kQ = 0, kK = 1, kV = 2 };
 // us, with two and six CTAs 160.
 __host__ __device__ constexpr int heads_at_a_time(int hc, bool append, int kind) { return append && kind == kK && hc == 4 ? 2 : hc; }
 
-// The rows of one kind.  An item: HC heads of one token, taken by one group of LPR lanes.  The cosines, the
-// weights and the token's place are fetched once for all of them, and the heads of a group's next item
-// are loaded while it works on this one: without that, 24 warps to an SM spend most of their time
-// waiting for the first of a chain of loads.
+// The rows of one kind.  A group of LPR lanes takes HC heads of one token at a time, and loads the heads of its next
+// round while it works on this one.  (One round to a warp, with all its loads after one another: video-DiT 211
+// us.)
 template <typename T, int LPR, int HC, int MODE, bool APPEND, int KIND>
 __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRows& k, unsigned cta, float* partner_buf) {
   constexpr unsigned kGroups = kThreads / LPR;
