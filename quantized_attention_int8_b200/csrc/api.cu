@@ -711,8 +711,7 @@ void set_norm_rope(HeadRowsParams* p, const sage_norm_rope& nr) {
   p->kind[0].weight = nr.q_weight, p->kind[1].weight = nr.k_weight, p->weight_dtype = nr.weight_dtype;
   p->vec_weight = p->d % 8 == 0 && aligned16(nr.q_weight) && aligned16(nr.k_weight);
   p->cos_sin = nr.cos_sin, p->n_pos = nr.n_pos, p->rot = nr.cos_sin ? nr.rot : 0, p->interleaved = nr.interleaved ? 1 : 0;
-  // a lane's pairs, four in a row, are all rotated or none is; its cosines and its sines are 16-byte vectors
-  if (nr.cos_sin) p->vec = p->vec && nr.rot % 8 == 0 && aligned16(nr.cos_sin);
+  if (nr.cos_sin && nr.rot % 8 == 0) p->vec = p->vec && aligned16(nr.cos_sin);  // angles are loaded four at a time
 }
 
 // Heads of a token that a group of lanes takes at a time: four (fewer instructions per row, more loads in

@@ -113,11 +113,13 @@ __device__ __forceinline__ void unpack8(const uint4& v, float2 (&x)[4]) {
 //   kWide    c .. c + 7, 16 bytes
 //   kHalves  a .. a + 3 and b .. b + 3, 8 bytes each: the same four places of the two rotated halves, or
 //            (behind the rotated channels) eight in a row
-enum Mode { kScalar, kWide, kHalves };
+//   kAny     as kWide, where the rotated channels are no multiple of eight: a lane's pairs are not its own, and
+//            partners and angles go through shared memory, as in kScalar
+enum Mode { kScalar, kWide, kHalves, kAny };
 
 template <int MODE>
 __device__ __forceinline__ uint4 load8(const unsigned short* row, int a, int b, int d) {
-  if (MODE == kWide) return a < d ? *reinterpret_cast<const uint4*>(row + a) : make_uint4(0, 0, 0, 0);
+  if (MODE == kWide || MODE == kAny) return a < d ? *reinterpret_cast<const uint4*>(row + a) : make_uint4(0, 0, 0, 0);
   if (MODE == kHalves) {
     const uint2 x = a < d ? *reinterpret_cast<const uint2*>(row + a) : make_uint2(0, 0);
     const uint2 y = b < d ? *reinterpret_cast<const uint2*>(row + b) : make_uint2(0, 0);
@@ -137,7 +139,7 @@ __device__ __forceinline__ void store8(unsigned short* row, int a, int b, int d,
   uint32_t w[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) w[e] = pack2(x[e].x, x[e].y, T());
-  if (MODE == kWide) {
+  if (MODE == kWide || MODE == kAny) {
     if (a < d && SAGE_STORE_OK(ext, row + a, 16, &g_cache_error))
       *reinterpret_cast<uint4*>(row + a) = make_uint4(w[0], w[1], w[2], w[3]);
   } else if (MODE == kHalves) {
@@ -292,9 +294,10 @@ __host__ __device__ constexpr int heads_at_a_time(int hc, bool append, int kind)
 // round while it works on this one.  (One round to a warp, with all its loads after one another: video-DiT 211
 // us.)
 template <typename T, int LPR, int HC, int MODE, bool APPEND, int KIND>
-__device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRows& k, unsigned cta, float* partner_buf) {
+__device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRows& k, unsigned cta, float* partner_buf,
+                                          float2* turns) {
   constexpr unsigned kGroups = kThreads / LPR;
-  constexpr bool kCoded = APPEND && KIND != kQ;
+  constexpr bool kCoded = APPEND && KIND != kQ, kShared = MODE == kScalar || MODE == kAny;
   const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
   const int half = p.rot >> 1;
   int a = lane * 8, b = a + 4;
@@ -342,7 +345,6 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
   unsigned token = ~0u;
   bool token_ok = false;
   float4 cs, sn;
-  const float* angles = p.cos_sin;  // (groups without an item read row 0 as well)
   uint8_t* codes = nullptr;
   float* scales = nullptr;
   const unsigned head_rows = 1u << p.map.page_log2, head_codes = head_rows * p.map.dc;  // of a page
@@ -398,8 +400,16 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
         atomicOr(&g_cache_error, kBadArg);
         token_ok = false;
       }
-      angles = p.cos_sin + (token_ok ? (long long)pos * p.rot : 0);
-      if (KIND != kV && MODE != kScalar && turn) {
+      const float* angles = p.cos_sin + (token_ok ? (long long)pos * p.rot : 0);
+      if (KIND != kV && kShared) {
+        if (p.cos_sin)
+#pragma unroll 1
+          for (int e = 0; e < 8; ++e) {  // this lane's own: no barrier
+            const int c = a + e, i = p.interleaved ? c >> 1 : c < half ? c : c - half;
+            if (c >= p.rot) break;
+            turns[e * kThreads + threadIdx.x] = make_float2(__ldg(angles + i), __ldg(angles + half + i));
+          }
+      } else if (KIND != kV && turn) {
         cs = __ldg(reinterpret_cast<const float4*>(angles + (MODE == kHalves ? a : a >> 1)));
         sn = __ldg(reinterpret_cast<const float4*>(angles + half + (MODE == kHalves ? a : a >> 1)));
       }
@@ -445,21 +455,21 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
           if (weights) x[e] = mul2(x[e], w[e]);
         }
       }
-      if (KIND != kV && MODE == kScalar) {
-        if (p.cos_sin) {  // uniform; the partners through shared memory
+      if (KIND != kV && kShared) {
+        if (p.cos_sin) {  // uniform
           float* buf = partner_buf + group * LPR * 8;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) buf[a + 2 * e] = x[e].x, buf[a + 2 * e + 1] = x[e].y;
+          for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(buf + a + 2 * e) = x[e];
           __syncwarp();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int c = a + e;
             if (c >= p.rot) continue;
             const bool low = p.interleaved ? !(c & 1) : c < half;
-            const int i_angle = p.interleaved ? c >> 1 : low ? c : c - half;
             const float y = buf[p.interleaved ? c ^ 1 : low ? c + half : c - half];
+            const float2 turn_e = turns[e * kThreads + threadIdx.x];
             float& z = e & 1 ? x[e >> 1].y : x[e >> 1].x;
-            z = z * __ldg(angles + i_angle) + (low ? -y : y) * __ldg(angles + half + i_angle);
+            z = z * turn_e.x + (low ? -y : y) * turn_e.y;
           }
           __syncwarp();
         }
@@ -512,7 +522,7 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
       if (odd && iv == 0.f) w0 = w1 = 0;
       if (live && (HC == 1 || h0 + i < k.H)) {
         uint8_t* const code = codes + (unsigned long long)(unsigned)(h0 + i) * head_codes;
-        const Extent& xc = KIND == kK ? p.x_k8 : p.x_v8;
+        [[maybe_unused]] const Extent& xc = KIND == kK ? p.x_k8 : p.x_v8;
         if (MODE == kHalves) {
           if (a < p.map.dc && SAGE_STORE_OK(xc, code + a, 4, &g_cache_error)) *reinterpret_cast<uint32_t*>(code + a) = w0;
           if (b < p.map.dc && SAGE_STORE_OK(xc, code + b, 4, &g_cache_error)) *reinterpret_cast<uint32_t*>(code + b) = w1;
@@ -534,13 +544,15 @@ __device__ __forceinline__ void head_rows(const HeadRowsParams& p, const HeadRow
 // 8192-token prompts 160 us, apart 209).
 template <typename T, int LPR, int HC, int MODE, bool APPEND>
 __global__ void __launch_bounds__(kThreads, HC > 1 ? 6 : 8) head_rows_kernel(const __grid_constant__ HeadRowsParams p) {
-  __shared__ float partner_buf[MODE == kScalar ? kThreads * 8 : 1];
+  constexpr int kShared = MODE == kScalar || MODE == kAny ? kThreads * 8 : 2;
+  __shared__ __align__(8) float partner_buf[kShared];
+  __shared__ float2 turns[kShared];  // cosine and sine of each lane's channels
   begin_dependent();
   const unsigned cta = blockIdx.x, q = p.apart ? p.kind[kQ].ctas : 0, k = p.apart ? q + p.kind[kK].ctas : 0;
-  if (!p.apart || cta < q) head_rows<T, LPR, HC, MODE, APPEND, kQ>(p, p.kind[kQ], cta, partner_buf);
-  if (!p.apart || (cta >= q && cta < k)) head_rows<T, LPR, heads_at_a_time(HC, APPEND, kK), MODE, APPEND, kK>(p, p.kind[kK], cta - q, partner_buf);
+  if (!p.apart || cta < q) head_rows<T, LPR, HC, MODE, APPEND, kQ>(p, p.kind[kQ], cta, partner_buf, turns);
+  if (!p.apart || (cta >= q && cta < k)) head_rows<T, LPR, heads_at_a_time(HC, APPEND, kK), MODE, APPEND, kK>(p, p.kind[kK], cta - q, partner_buf, turns);
   if (APPEND && (!p.apart || cta >= k))
-    head_rows<T, LPR, HC, MODE == kHalves ? kWide : MODE, APPEND, kV>(p, p.kind[kV], cta - k, partner_buf);
+    head_rows<T, LPR, HC, MODE == kScalar ? kScalar : kWide, APPEND, kV>(p, p.kind[kV], cta - k, partner_buf, turns);
 }
 
 // ------------------------------------------------------------------------------------------ read back
@@ -672,6 +684,8 @@ cudaError_t launch_rows(HeadRowsParams p, cudaStream_t st) {
 template <typename T, int LPR>
 cudaError_t launch_rows_lpr(const HeadRowsParams& p, cudaStream_t st) {
   if (!p.vec) return launch_rows<T, LPR, 1, kScalar>(p, st);
+  if (p.cos_sin && p.rot % 8 != 0)
+    return p.heads_per_group == 4 ? launch_rows<T, LPR, 4, kAny>(p, st) : launch_rows<T, LPR, 1, kAny>(p, st);
   if (p.cos_sin && !p.interleaved)
     return p.heads_per_group == 4 ? launch_rows<T, LPR, 4, kHalves>(p, st) : launch_rows<T, LPR, 1, kHalves>(p, st);
   return p.heads_per_group == 4 ? launch_rows<T, LPR, 4, kWide>(p, st) : launch_rows<T, LPR, 1, kWide>(p, st);

@@ -28,6 +28,8 @@ ROWS = [  # layout, B, N, Hq, Hkv, d, rot, dtype, norm, weights, interleaved
     ("packed", 1, 400, 32, 8, 128, 128, BF16, True, "same", False),  # groups of four heads
     ("HND", 2, 1000, 9, 3, 64, 64, F16, True, "fp32", False),    # groups of four, the last of one head
     ("packed", 1, 3, 2, 2, 130, 2, BF16, True, "same", False),
+    ("NHD", 1, 2400, 32, 32, 40, 20, F16, True, "fp32", False),  # rotated channels that are no multiple of eight,
+    ("HND", 2, 1201, 32, 32, 48, 20, BF16, True, "same", True),  # four heads at a time
 ]
 
 
@@ -222,6 +224,7 @@ FUSED = [  # d, rot, Hq, Hkv, dtype, norm, interleaved, k_mean, lengths before, 
     (40, 40, 4, 2, BF16, True, False, False, [0, 1], [5, 17]),                 # the scalar path
     (256, 128, 4, 4, F16, True, False, False, [9], [20]),
     (64, 0, 4, 1, F16, True, False, False, [0], [30]),                        # norm alone
+    (40, 20, 16, 8, BF16, True, False, True, [0, 50], [2000, 700]),           # halves of 10, four heads at a time
     (128, 128, 32, 8, F16, True, False, True, [0, 100], [700, 400]),          # groups of four heads
 ]
 
