@@ -299,7 +299,7 @@ typedef struct {
  * With nr, the keys are normed and rotated as by sage_qk_norm_rope at their position in the sequence first
  * (fp32 up to the code), and so is q (T, Hq, d) into q_out; without q (NULL) Hq is ignored.  nr NULL: k is
  * coded as it is, and q must be NULL.  strides: 8 element strides >= 0, of the tokens and heads of q, k, v and
- * q_out.  q_out may be q.  A token whose position is negative, beyond the page table or (with nr) not in
+ * q_out.  q_out may be q, and must not overlap the cache.  A token whose position is negative, beyond the page table or (with nr) not in
  * cos_sin is skipped and reported like a bad page.  Two tokens must not have the same place: where two
  * sequences of one call share the page that both write, that place holds codes of either.
  * T = 0 does nothing.  Allocates nothing. */
@@ -318,7 +318,8 @@ sage_status sage_cache_gather(const sage_kv_cache* cache, const int32_t* page_ta
 
 /* Attention of one query token per sequence over its cached tokens:
  *   out = softmax(q . K * sm_scale) V,  K = code * ks, V = code * vs
- * q: (B, Hq, d) with element strides q_batch_stride and q_head_stride, out: (B, Hq, d) contiguous, of q's dtype.
+ * q: (B, Hq, d) with element strides q_batch_stride and q_head_stride, out: (B, Hq, d) contiguous, of q's dtype;
+ * it must not overlap q or the cache.
  * q is not quantized: scores, softmax and sums are fp32 on exact products of q and the codes.  seq_lens: DEVICE
  * int32 [B], the keys each query sees (the new token's own key among them if it was appended); 0 gives zeros.
  * max_seqlen >= 0 bounds them; a sequence longer than it or than its page table, or of negative length, is

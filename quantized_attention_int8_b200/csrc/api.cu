@@ -678,6 +678,12 @@ sage_status check_cache(const sage_kv_cache* c, const int32_t* table, long long 
 
 size_t cache_rows(const PageMap& m) { return ((size_t)m.num_pages * m.Hkv) << m.page_log2; }
 
+bool overlaps_cache(const void* p, size_t n, const PageMap& m) {
+  const size_t scales = cache_rows(m) * 4, codes = cache_rows(m) * m.dc;
+  return overlaps(p, n, m.k8, codes) || overlaps(p, n, m.v8, codes) || overlaps(p, n, m.ks, scales) ||
+         overlaps(p, n, m.vs, scales);
+}
+
 bool view_fits(const HeadView& v, long long B, long long N, long long H) {
   const auto fits = [](long long n, long long stride) { return stride == 0 || (n - 1) <= kMaxExtent / stride; };
   return fits(B, v.batch) && fits(N, v.token) && fits(H, v.head);
@@ -815,13 +821,9 @@ sage_status sage_cache_gather(const sage_kv_cache* cache, const int32_t* page_ta
   if (((uintptr_t)k_mean | (uintptr_t)starts | (uintptr_t)cu_seqlens) & 3) return SAGE_ERR_INVALID_ARG;
   if (T == 0 || B == 0) return SAGE_OK;
   if (!cu_seqlens || !k_out || !v_out || (((uintptr_t)k_out | (uintptr_t)v_out) & 1)) return SAGE_ERR_INVALID_ARG;
-  const size_t bytes = (size_t)T * cache->Hkv * cache->d * 2, codes = cache_rows(p.map) * p.map.dc;
-  const size_t scales = cache_rows(p.map) * 4;
-  if (overlaps(k_out, bytes, v_out, bytes)) return SAGE_ERR_INVALID_ARG;
-  for (const void* o : {(const void*)k_out, (const void*)v_out})
-    if (overlaps(o, bytes, cache->k8, codes) || overlaps(o, bytes, cache->v8, codes) ||
-        overlaps(o, bytes, cache->ks, scales) || overlaps(o, bytes, cache->vs, scales))
-      return SAGE_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)T * cache->Hkv * cache->d * 2;
+  if (overlaps(k_out, bytes, v_out, bytes) || overlaps_cache(k_out, bytes, p.map) || overlaps_cache(v_out, bytes, p.map))
+    return SAGE_ERR_INVALID_ARG;
   p.cu = cu_seqlens, p.starts = starts, p.k_mean = k_mean, p.k_out = k_out, p.v_out = v_out;
   p.B = B, p.T = T, p.d = cache->d;
   const int hkv = cache->Hkv;
@@ -852,7 +854,8 @@ sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long 
     return SAGE_ERR_INVALID_ARG;
   p.q = HeadView{q, q_batch_stride, 0, q_head_stride};
   const size_t out_bytes = (size_t)B * Hq * cache->d * 2;
-  if (overlaps(out, out_bytes, q, view_bytes(p.q, B, 1, Hq, cache->d))) return SAGE_ERR_INVALID_ARG;
+  if (overlaps(out, out_bytes, q, view_bytes(p.q, B, 1, Hq, cache->d)) || overlaps_cache(out, out_bytes, p.map))
+    return SAGE_ERR_INVALID_ARG;
   p.out = out, p.seq_lens = seq_lens;
   p.B = B, p.Hq = Hq, p.G = Hq / cache->Hkv, p.d = cache->d;
   p.tiles = (p.G + kDecodeHeads - 1) / kDecodeHeads;

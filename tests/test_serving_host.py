@@ -125,6 +125,18 @@ def test_append_gather_decode_argument_checks(lib, no_device):
         assert _decode(lib, **kw) == E, kw
 
 
+@pytest.mark.parametrize("array", ["k8", "ks", "v8", "vs"])
+def test_decode_refuses_an_output_inside_the_cache(lib, no_device, array):
+    at = {name: FAKE + ((i + 2) << 32) for i, name in enumerate(("k8", "ks", "v8", "vs"))}
+    rows = 4 * 2 * 64                                          # pages, kv heads, page_size
+    size = rows * (64 if array in ("k8", "v8") else 4)
+    out_bytes = 2 * 4 * 64 * 2
+    for out, want in ((at[array], lib.SAGE_ERR_INVALID_ARG), (at[array] + size - 2, lib.SAGE_ERR_INVALID_ARG),
+                      (at[array] - out_bytes + 2, lib.SAGE_ERR_INVALID_ARG),
+                      (at[array] + size, no_device), (at[array] - out_bytes, no_device)):
+        assert _decode(lib, _cache(lib, **at), out=out) == want, (array, out - at[array])
+
+
 def test_decode_reports_a_failed_workspace(lib):
     try:
         lib.capi.sage_test_inject(100, 1)  # one long sequence: split, so it needs a workspace
