@@ -603,6 +603,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) decode_join_kernel(const _
   constexpr int kBatch = kJoinBatch / V;
   __shared__ float4 sm_o[kJoinWarps][32 * V];
   const Place at = find_place<kJoinWarps * 32>(p, blockIdx.x + 1, false);
+  // Every CTA waits, those without a border too: where none had to, this grid would end before the other, and what
+  // follows it in the stream is ordered behind this grid alone.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (at.b < 0) return;
   const uint32_t u = (blockIdx.x + 1) * at.share, keys0 = at.pair0 + p.unit_extra;
   if (u <= keys0 || u - at.share > keys0) return;  // no pair's keys cross here, or they crossed an earlier border
@@ -613,7 +616,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) decode_join_kernel(const _
   const int head = min(warp / ways, nheads - 1), way = warp % ways;
   // CTA c's part: its last pair's (1) where the pair began, its first one's (0) behind that
   const auto part = [&](int i) { return (long long)((c0 + i) * 2 + (i == 0 ? 1 : 0)) * kHeads + head; };
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   float top = -FLT_MAX, sum = 0.f;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(ml + part(i)).x);

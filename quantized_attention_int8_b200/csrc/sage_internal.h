@@ -240,7 +240,10 @@ struct DecodeParams {
 };
 
 // Launches a kernel as a programmatic dependent of the one before it in the stream: its CTAs may be set up while
-// that one ends.  The kernel calls griddepcontrol.wait before it touches memory.
+// that one ends.  Every CTA calls griddepcontrol.wait, on every way out, and before it touches memory that work
+// before it writes or reads: a grid whose CTAs did not could end first, and let later work past what it depends on.
+// (The join of the one-token attention reads the lengths before it waits: the kernel before it only reads them
+// too, and lets it in after its own wait.)
 template <typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
                              const Args&... args) {
