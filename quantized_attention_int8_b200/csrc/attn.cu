@@ -111,6 +111,10 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
 __device__ __forceinline__ void store_elem(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Waits for the grid before this one in the stream.  Where no CTA of a grid called it (a packed batch without keys), the grid
+// could end first, and what comes behind it in the stream is ordered behind this grid alone.
+__device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Warp-uniform bounded wait: every lane waits, and the warp proceeds only if all did.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const bool ok = mbar_wait(bar, parity, abort);
@@ -182,7 +186,10 @@ __global__ void __launch_bounds__(192, FwdCfg<DQK, DV, PV16>::CTAS_PER_SM)
   const int nblk_q = (nq + 127) / 128;
   int qt = blockIdx.x;
   if (CAUSAL) qt = nblk_q - 1 - qt;  // longest rows first
-  if (qt < 0 || qt >= nblk_q) return;  // past the end of this sequence (the whole CTA leaves)
+  if (qt < 0 || qt >= nblk_q) {  // past the end of this sequence (the whole CTA leaves)
+    if (PACKED) wait_for_previous_grid();
+    return;
+  }
   const int hq = blockIdx.y;
   const int hkv = hq / p.G;
   // Causal mask, bottom-right aligned: query i sees keys j <= i + (nk - nq).
@@ -198,6 +205,7 @@ __global__ void __launch_bounds__(192, FwdCfg<DQK, DV, PV16>::CTAS_PER_SM)
   const long long orow = sv.q_in + (long long)grow * sv.q_tok + (long long)hq * sv.q_head;  // output row start
   if (n_kv == 0) {
     // no row of this tile sees a key (nk = 0, or the causal offset leaves the tile empty): zeros
+    if (PACKED) wait_for_previous_grid();  // (of a dense batch the last tile sees keys, and waits)
     if (warp < 4 && grow < nq)
       for (int c = 0; c < p.m.d; ++c)
         if (SAGE_STORE_OK(p.x_out, out + orow + c, sizeof(OutT), &g_device_error)) store_elem(out + orow + c, 0.f);
@@ -206,7 +214,7 @@ __global__ void __launch_bounds__(192, FwdCfg<DQK, DV, PV16>::CTAS_PER_SM)
 
   // launched as a programmatic dependent of the quantize pass: wait for it to finish (and its
   // codes and scales to be visible) before anything below reads them
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous_grid();
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     for (int s = 0; s < C::ST; ++s) {

@@ -45,7 +45,7 @@ cudaError_t read_clear_quant_error(int* value) {
 }
 
 // Programmatic dependent launch: the finalize and pass-2 grids are launched while their
-// predecessor still runs; they wait here for it to complete (and its writes to be visible)
+// predecessor still runs; all their CTAs wait here for it to complete (and its writes to be visible)
 // before reading what it wrote.
 __device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -615,8 +615,8 @@ __global__ void __launch_bounds__(256, 2) quant_pass2_kernel(QuantParams p) {
   const long long tstride = sv.k_tok;
   const bool vec = isk ? p.vec_k : p.vec_v;
   const int blk0 = (gridDim.x - 1 - blockIdx.x) * p.bpc, blk1 = min((sv.nk + 127) / 128, blk0 + p.bpc);
-  if (blk0 >= blk1) return;  // past the end of this sequence (the whole CTA leaves)
   wait_for_previous_grid();  // pass 1's partials (p.fold), or the finalize kernel's K mean and V scales
+  if (blk0 >= blk1) return;  // past the end of this sequence (the whole CTA leaves)
   // Short sequences (p.fold): no finalize launch; every CTA computes its head's K mean, or V's
   // scales and mean, from pass 1's partials in the same order, and the head's first CTA writes
   // them out.  Otherwise the finalize kernel has written them.

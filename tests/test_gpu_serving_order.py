@@ -57,3 +57,20 @@ def test_short_sequences_under_a_large_bound(lib, B, n, bound, captured):
     for j, ts in enumerate(got):
         for a, b in zip(ts, want[j % 2]):
             assert torch.equal(S.bits(a), S.bits(b)), j
+
+
+def test_a_packed_batch_without_keys_before_other_calls(lib):
+    """Queries that see no key get zeros, and the passes behind the first have nothing to do: the call's workspace, and the
+    queries that the first pass reads, belong to the next call only when that pass has ended."""
+    H, d, n = 16, 128, 8192
+    q = S.heads((4 * n, H, d), F16, 0).cuda()
+    none = torch.zeros((1, H, d), dtype=F16, device="cuda")  # a row that no sequence owns
+    cu = torch.arange(0, 4 * n + 1, n, dtype=torch.int32, device="cuda")
+    x = [S.heads((1, H, 1024, d), F16, i).cuda() for i in range(1, 4)]
+    want = lib.sage_attn(*x)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        zeros = lib.sage_attn_varlen(q, none, none, cu, torch.zeros_like(cu), n, 0)
+        got = lib.sage_attn(*x)
+        assert torch.equal(S.bits(got), S.bits(want)) and not zeros.any()
+    lib.sage_check_status()
