@@ -881,6 +881,7 @@ sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long 
   p.unit_extra = 0, p.unit_log2 = p.max_len <= 512 ? 9 : 8;
   if (p.unit_log2 == 8 && units() > most) p.unit_extra = p.d <= 64 ? 8 : p.d <= 128 ? 6 : 4, p.unit_log2 = 6;
   while (units() >= (1LL << 31) && p.unit_log2 < 30) ++p.unit_log2;
+  if (p.max_len <= 1 << p.unit_log2) p.unit_extra = 0;  // one unit to every pair: nothing is shared out
   if (units() >= (1LL << 31)) return SAGE_ERR_INVALID_ARG;
   const bool split = p.max_len > 1 << p.unit_log2;  // a pair may cross CTAs
   p.ctas = (uint32_t)(split ? std::min<long long>(units(), most) : units());
