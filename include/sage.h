@@ -320,7 +320,10 @@ sage_status sage_cache_gather(const sage_kv_cache* cache, const int32_t* page_ta
  *   out = softmax(q . K * sm_scale) V,  K = code * ks, V = code * vs
  * q: (B, Hq, d) with element strides q_batch_stride and q_head_stride, out: (B, Hq, d) contiguous, of q's dtype;
  * it must not overlap q or the cache.
- * q is not quantized: scores, softmax and sums are fp32 on exact products of q and the codes.  seq_lens: DEVICE
+ * q is not quantized: scores and their sum are fp32 on exact products of q and the codes (a bf16 value of q below 2^-29
+ * of its head's largest is rounded to 2^-40 of that).  The weights that V's codes are multiplied with are rounded, to
+ * 2^-11 of themselves for bf16 and 2^-22 for fp16, and no finer than 2^-36 of the largest among the keys of a
+ * warp; those products are exact and summed in fp32.  seq_lens: DEVICE
  * int32 [B], the keys each query sees (the new token's own key among them if it was appended); 0 gives zeros.
  * max_seqlen >= 0 bounds them; a sequence longer than it or than its page table, or of negative length, is
  * reported by sage_check_status as SAGE_ERR_INVALID_ARG and gets zeros; keys on a bad page are left out and

@@ -26,7 +26,8 @@
 //   * the scores' C layout becomes P^T's B layout by one 8x8 transpose (movmatrix) per 8 keys.
 //
 // V's scale is folded into the weights: w_j = s_j + log2(vs_j) has a running reference of its own, so
-// the fp16 weights 2^(w_j - ref) keep their precision whatever the scales' spread; the sum uses s_j.
+// that the spread of the scales takes nothing from the fp16 weights 2^(w_j - ref); the sum uses s_j, in fp32.
+// What the 16 bits of the weights cost: see kLift, and the second term of fp16 outputs.
 #include <atomic>
 #include <cfloat>
 #include <type_traits>
@@ -54,7 +55,12 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kHeads = kDecodeHeads;  // query heads per tile (N of the products)
 constexpr int kTimeout = 1, kBadArg = 2;  // the error word's bits for SAGE_ERR_TIMEOUT and SAGE_ERR_INVALID_ARG
-constexpr float kLag = 8.f;     // the reference moves when a score passes it by 2^8: a weight stays below 2^8 in fp16
+// The references of the running softmax (log2 units): the sum's moves when a score passes it by kLag.  The weights
+// of P V are fp16 and stand kLift above theirs (the largest seen when it moved), so that they stay below 2^15 and
+// are lost (below 2^-25) only kLift + 25 powers of two under it: n such keys of a warp, whatever they hold together,
+// are off by n 2^-36 of the warp's largest weight.  At 8 and 0, keys 25 powers of two below a
+// dominant one vanished from O and counted in the sum.
+constexpr float kLag = 4.f, kLift = 11.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
       for (int m = 0; m < VC * VW * 2; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[m][e] = 0.f;
-      float ms[2] = {-FLT_MAX, -FLT_MAX}, mw[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
+      float ms[2] = {-FLT_MAX, -FLT_MAX}, mw[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};  // (mw: less kLift)
 
       const int krow = (4 * (g >> 1) + (g & 1));  // key of S's row g; two more for row g + 8
       const unsigned char* const k_lane = ring + krow * dc + 16 * t;
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            move |= fmaxf(s[x][h], s[x][2 + h]) > ms[h] + kLag || fmaxf(w[x][h], w[x][2 + h]) > mw[h] + kLag;
+            move |= fmaxf(s[x][h], s[x][2 + h]) > ms[h] + kLag || fmaxf(w[x][h], w[x][2 + h]) > mw[h] + (kLag + kLift);
         }
         if (__any_sync(0xffffffffu, move)) {
           float f[2];
@@ -470,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
 #pragma unroll
             for (int x = 1; x < R::kTiles; ++x)
               ts = fmaxf(ts, fmaxf(s[x][h], s[x][2 + h])), tw = fmaxf(tw, fmaxf(w[x][h], w[x][2 + h]));
-            const float nms = fmaxf(ms[h], max_over_keys(ts)), nmw = fmaxf(mw[h], max_over_keys(tw));
+            const float nms = fmaxf(ms[h], max_over_keys(ts)), nmw = fmaxf(mw[h], max_over_keys(tw) - kLift);
             l[h] *= ex2(ms[h] - nms);
             f[h] = ex2(mw[h] - nmw);
             ms[h] = nms, mw[h] = nmw;
@@ -480,8 +486,10 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[m][e] *= f[e & 1];
         }
-        // P^T as B operand: fp16.  For fp16 outputs a second fp16 term carries what the first rounds off
-        // (2^-12 of a weight would be as large as the output's own rounding).
+        // P^T as B operand: fp16, a weight off by up to 2^-11 of itself.  For bf16 outputs that is enough: an eighth of
+        // their own rounding (2^-8) if all weights were off the same way.  For fp16 outputs it would be as large as
+        // theirs, and a second fp16 term carries what the first rounds off (2^-22 is left; B32 L16384 Hq32 Hkv8 d128
+        // takes 202 us with it and 186 without).
         uint32_t ph[R::kTiles][2], pl[R::kTiles][2];
 #pragma unroll
         for (int x = 0; x < R::kTiles; ++x) {
@@ -548,13 +556,13 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 2 : 3) decode_kernel(Dec
         float top = sm_m[0][head];
 #pragma unroll
         for (int x = 1; x < kWarps; ++x) top = fmaxf(top, sm_m[x][head]);
-        const float f = ex2(mw[h] - top);
+        const float f = ex2(mw[h] + kLift - top), drop = 1.f / (1 << (int)kLift);  // (apart: their product may be subnormal)
 #pragma unroll
         for (int q = 0; q < VC; ++q)
 #pragma unroll
           for (int m = 0; m < VW * 2; ++m) {
             float* dst = sm_o + (warp * kHeads + head) * DP + 8 * VP * q + VP * g + 2 * m;
-            *reinterpret_cast<float2*>(dst) = make_float2(o[q * VW * 2 + m][h] * f, o[q * VW * 2 + m][2 + h] * f);
+            *reinterpret_cast<float2*>(dst) = make_float2(o[q * VW * 2 + m][h] * drop * f, o[q * VW * 2 + m][2 + h] * drop * f);
           }
       }
       __syncthreads();
