@@ -260,7 +260,9 @@ typedef struct {
  * projection among them.  positions: DEVICE int32 [B][N], rows pos_batch_stride elements apart (0: one row
  * for all batches); NULL: token n is at position n.  A token whose position is not in 0 .. n_pos - 1 is
  * left unwritten, and sage_check_status returns SAGE_ERR_INVALID_ARG.  q_out may be q and k_out may be k
- * (same pointer and strides); outputs must not share other elements with an input or each other.
+ * (same pointer and strides); outputs must not share other elements with an input, each other or themselves
+ * (SAGE_ERR_INVALID_ARG for q, k and the outputs; views whose extents overlap have to be slices side by side of rows of one
+ * length, like the heads of a fused projection, in any layout).
  * N = 0 or B = 0 does nothing.  Allocates nothing. */
 sage_status sage_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
                               const int32_t* positions, long long pos_batch_stride, int B, int N, int Hq, int Hkv,
@@ -299,7 +301,8 @@ typedef struct {
  * With nr, the keys are normed and rotated as by sage_qk_norm_rope at their position in the sequence first
  * (fp32 up to the code), and so is q (T, Hq, d) into q_out; without q (NULL) Hq is ignored.  nr NULL: k is
  * coded as it is, and q must be NULL.  strides: 8 element strides >= 0, of the tokens and heads of q, k, v and
- * q_out.  q_out may be q, and must not overlap the cache.  A token whose position is negative, beyond the page table or (with nr) not in
+ * q_out.  q_out may be q, and must not overlap the cache, k or v, or in another way q (as for
+ * sage_qk_norm_rope).  A token whose position is negative, beyond the page table or (with nr) not in
  * cos_sin is skipped and reported like a bad page.  Two tokens must not have the same place: where two
  * sequences of one call share the page that both write, that place holds codes of either.
  * T = 0 does nothing.  Allocates nothing. */

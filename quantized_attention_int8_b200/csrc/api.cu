@@ -694,6 +694,70 @@ size_t view_bytes(const HeadView& v, long long B, long long N, long long H, long
   return (size_t)((B - 1) * v.batch + (N - 1) * v.token + (H - 1) * v.head + d) * 2;
 }
 
+// Whether a place can belong to both views (conservative).  They are apart where their extents are, and where they
+// are slices side by side of rows S elements apart, S one of the strides: every larger stride in use a multiple of S, and what the
+// others span disjoint modulo S (q and k of one fused projection).
+bool views_overlap(const HeadView& a, const long long na[3], const HeadView& b, const long long nb[3], long long d) {
+  const long long sa[3] = {a.batch, a.token, a.head}, sb[3] = {b.batch, b.token, b.head};
+  if (!overlaps(a.ptr, view_bytes(a, na[0], na[1], na[2], d), b.ptr, view_bytes(b, nb[0], nb[1], nb[2], d))) return false;
+  const long long apart = ((long long)(uintptr_t)b.ptr - (long long)(uintptr_t)a.ptr) / 2;  // (both addresses are even)
+  for (const long long S : sa) {
+    if (S == 0) continue;
+    long long span[2] = {d, d};  // elements of the dimensions inside a row
+    bool rows = true;
+    for (int i = 0; i < 3; ++i) {
+      const long long n[2] = {na[i], nb[i]}, s[2] = {sa[i], sb[i]};
+      for (int x = 0; x < 2; ++x) {
+        if (n[x] == 1) continue;
+        if (s[x] < S)
+          span[x] += (n[x] - 1) * s[x];
+        else
+          rows = rows && s[x] % S == 0;
+      }
+    }
+    const long long at = ((apart % S) + S) % S;  // of b's first element in a's row
+    if (rows && at >= span[0] && at + span[1] <= S) return false;
+  }
+  return true;
+}
+
+bool same_view(const HeadView& a, const HeadView& b, const long long n[3]) {
+  return a.ptr == b.ptr && (n[0] == 1 || a.batch == b.batch) && (n[1] == 1 || a.token == b.token) &&
+         (n[2] == 1 || a.head == b.head);
+}
+
+// Whether two elements of a view can share a place (conservative): its strides in use, in order of size, each pass over
+// what the smaller ones span.
+bool overlaps_itself(const HeadView& v, const long long n[3], long long d) {
+  long long s[3] = {v.batch, v.token, v.head}, m[3] = {n[0], n[1], n[2]}, span = d;
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[j] < s[i]) std::swap(s[i], s[j]), std::swap(m[i], m[j]);
+  for (int i = 0; i < 3; ++i) {
+    if (m[i] == 1) continue;
+    if (s[i] < span) return true;
+    span += (m[i] - 1) * s[i];
+  }
+  return false;
+}
+
+// Outputs may be their own inputs; otherwise no output shares a place with a view that is read, another output
+// or itself.  (Rows of one kind are written while others are read.)
+sage_status check_apart(const HeadRowsParams& p, int batches) {
+  for (const HeadRows& o : p.kind) {
+    if (!o.H || !o.out.ptr) continue;
+    const long long no[3] = {batches, p.N, o.H};
+    if (overlaps_itself(o.out, no, p.d)) return SAGE_ERR_INVALID_ARG;
+    for (const HeadRows& k : p.kind) {
+      if (!k.H) continue;
+      const long long nk[3] = {batches, p.N, k.H};
+      if (!(&k == &o && same_view(o.out, k.in, no)) && views_overlap(o.out, no, k.in, nk, p.d)) return SAGE_ERR_INVALID_ARG;
+      if (&k != &o && k.out.ptr && views_overlap(o.out, no, k.out, nk, p.d)) return SAGE_ERR_INVALID_ARG;
+    }
+  }
+  return SAGE_OK;
+}
+
 // 16-byte vectors: the base aligned and every stride in use a multiple of eight elements.
 bool vec_view(const HeadView& v, long long B, long long N, long long H) {
   return aligned16(v.ptr) && (B == 1 || v.batch % 8 == 0) && (N == 1 || v.token % 8 == 0) &&
@@ -771,6 +835,7 @@ sage_status sage_qk_norm_rope(const void* q, const void* k, void* q_out, void* k
   set_norm_rope(&p, *nr);
   if ((s = shape_rows(&p, B)) != SAGE_OK) return s;
   if ((s = check_device()) != SAGE_OK) return s;
+  if ((s = check_apart(p, B)) != SAGE_OK) return s;
   return from_cuda(launch_head_rows(p, dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -806,6 +871,8 @@ sage_status sage_cache_append(const sage_kv_cache* cache, const void* q, const v
   p.x_ks = extent_of(cache->ks, rows * 4), p.x_vs = extent_of(cache->vs, rows * 4);
   if ((s = shape_rows(&p, 1)) != SAGE_OK) return s;
   if ((s = check_device()) != SAGE_OK) return s;
+  if ((s = check_apart(p, 1)) != SAGE_OK) return s;
+  if (q && overlaps_cache(q_out, view_bytes(p.kind[0].out, 1, T, Hq, d), p.map)) return SAGE_ERR_INVALID_ARG;
   return from_cuda(launch_head_rows(p, dtype, static_cast<cudaStream_t>(stream)));
 }
 
