@@ -23,6 +23,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import sys
 
 import torch
 
@@ -38,8 +39,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsage_b20
 # the same library compiled with -DSAGE_CHECKED: every kernel store tests its extent first
 CHECKED_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsage_b200_checked.so")
 
-# the compiled binding of the serving calls (csrc/binding.cpp)
-BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_sage_binding.so")
+# the compiled binding of the serving calls (csrc/binding.cpp), of this Python and this torch; loaded by the first of them
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
+                            f"_sage_binding.{sys.implementation.cache_tag}-torch{torch.__version__}.so")
 
 SAGE_OK, SAGE_ERR_INVALID_ARG, SAGE_ERR_UNSUPPORTED, SAGE_ERR_ARCH, SAGE_ERR_CUDA, SAGE_ERR_OOM, \
     SAGE_ERR_TIMEOUT, SAGE_ERR_BOUNDS = range(8)
@@ -138,17 +140,24 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
-def _load_binding(path: str = BINDING_PATH):
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is not built; run `python quantized_attention_int8_b200/build_lib.py`")
-    spec = importlib.util.spec_from_file_location("_sage_binding", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    return module
+_binding = None
+
+
+def _serving():
+    """The compiled binding, loaded on first use: nothing else in the package needs it."""
+    global _binding
+    if _binding is None:
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(f"{BINDING_PATH} is not built; run `python quantized_attention_int8_b200/build_lib.py` "
+                              "(the serving calls need it)")
+        spec = importlib.util.spec_from_file_location("_sage_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding = module
+    return _binding
 
 
 capi = _load()
-_binding = _load_binding()
 
 
 def load_checked() -> ctypes.CDLL:
@@ -325,8 +334,8 @@ def sage_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weigh
     bf16 or fp32.  q_out may be q and k_out may be k."""
     if tensor_layout not in _LAYOUTS:
         raise ValueError(f"tensor_layout must be 'HND' or 'NHD', got {tensor_layout!r}")
-    r = _binding.qk_norm_rope(capi.serving["sage_qk_norm_rope"], q, k, positions, tensor_layout == "HND", cos_sin,
-                              q_weight, k_weight, norm, eps, interleaved, q_out, k_out)
+    r = _serving().qk_norm_rope(capi.serving["sage_qk_norm_rope"], q, k, positions, tensor_layout == "HND", cos_sin,
+                                q_weight, k_weight, norm, eps, interleaved, q_out, k_out)
     if type(r) is int:
         _check(r, "sage_qk_norm_rope")
     return r
@@ -353,9 +362,9 @@ def sage_cache_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, q=None
     which is returned (q_out; None without q).  k_mean float32 (Hkv,d) is subtracted from the keys before
     they are coded.  Channels contiguous, other strides free.  Bad pages and positions are skipped and reported
     by sage_check_status."""
-    r = _binding.cache_append(capi.serving["sage_cache_append"], cache["k8"], cache["ks"], cache["v8"], cache["vs"], k, v,
-                              page_table, seq_lens, cu_seqlens, q, cos_sin, q_weight, k_weight, norm, eps, interleaved,
-                              k_mean, q_out)
+    r = _serving().cache_append(capi.serving["sage_cache_append"], cache["k8"], cache["ks"], cache["v8"], cache["vs"], k, v,
+                                page_table, seq_lens, cu_seqlens, q, cos_sin, q_weight, k_weight, norm, eps, interleaved,
+                                k_mean, q_out)
     if type(r) is int:
         _check(r, "sage_cache_append")
     return r
@@ -369,8 +378,8 @@ def sage_cache_gather(cache, page_table, cu_seqlens, total, head_dim, dtype=torc
     code = _DTYPES.get(dtype)
     if code is None:
         raise ValueError(f"unsupported dtype {dtype}")
-    r = _binding.cache_gather(capi.serving["sage_cache_gather"], cache["k8"], cache["ks"], cache["v8"], cache["vs"],
-                              page_table, cu_seqlens, total, head_dim, code, starts, k_mean, k_out, v_out)
+    r = _serving().cache_gather(capi.serving["sage_cache_gather"], cache["k8"], cache["ks"], cache["v8"], cache["vs"],
+                                page_table, cu_seqlens, total, head_dim, code, starts, k_mean, k_out, v_out)
     if type(r) is int:
         _check(r, "sage_cache_gather")
     return r
@@ -381,8 +390,8 @@ def sage_attn_decode(q, cache, page_table, seq_lens, max_seqlen, sm_scale=None, 
 
     seq_lens int32 (B,): the cached keys each query sees (0: zeros); max_seqlen bounds them (a longer sequence gets
     zeros and is reported by sage_check_status).  q may be strided (channels contiguous)."""
-    r = _binding.attn_decode(capi.serving["sage_attn_decode"], cache["k8"], cache["ks"], cache["v8"], cache["vs"], q,
-                             page_table, seq_lens, max_seqlen, 0.0 if sm_scale is None else sm_scale, out)
+    r = _serving().attn_decode(capi.serving["sage_attn_decode"], cache["k8"], cache["ks"], cache["v8"], cache["vs"], q,
+                               page_table, seq_lens, max_seqlen, 0.0 if sm_scale is None else sm_scale, out)
     if type(r) is int:
         _check(r, "sage_attn_decode")
     return r

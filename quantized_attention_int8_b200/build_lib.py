@@ -1,8 +1,10 @@
 """Builds the CUDA library in-tree with nvcc for sm_100a: libsage_b200.so and its checked
 twin libsage_b200_checked.so (-DSAGE_CHECKED: every kernel store tests its extent first); and
-_sage_binding.so, the serving calls' Python binding (host code against torch's headers).
+_sage_binding.<python>-torch<version>.so, the serving calls' Python binding (host code against torch's headers).
 
-Usage: python quantized_attention_int8_b200/build_lib.py [--force] [--ptxas-info] [--no-checked]
+Usage: python quantized_attention_int8_b200/build_lib.py [--force] [--ptxas-info] [--no-checked] [--no-binding]
+
+Without the binding the package has everything but the serving calls.
 
 Run it as a script (not as a module of the package): importing the package
 loads the library, which may not exist yet or may be stale.
@@ -21,7 +23,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsage_b200.so")
 LIB_CHECKED = os.path.join(PKG, "libsage_b200_checked.so")
-BINDING = os.path.join(PKG, "_sage_binding.so")
 SOURCES = ["api.cu", "attn.cu", "quant.cu", "cache.cu", "decode.cu"]
 HEADERS = ["sm100.cuh", "sage_internal.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -63,14 +64,16 @@ def _build_one(lib: str, defines: list[str], force: bool, ptxas_info: bool, verb
 
 
 def _build_binding(force: bool, verbose: bool) -> None:
-    if not force and not _stale(BINDING, ["binding.cpp"]):
-        return
     import torch
+    # named for the Python and the torch that it is built against: another one looks for a file of its own
+    binding = os.path.join(PKG, f"_sage_binding.{sys.implementation.cache_tag}-torch{torch.__version__}.so")
+    if not force and not _stale(binding, ["binding.cpp"]):
+        return
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    tmp = BINDING + ".tmp"
+    tmp = binding + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
            *[x for i in includes for x in ("-isystem", i)], "-o", tmp, os.path.join(CSRC, "binding.cpp"),
@@ -80,18 +83,21 @@ def _build_binding(force: bool, verbose: bool) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, binding)
 
 
-def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False, checked: bool = True) -> str:
-    """Builds the library (and, unless checked=False, its checked twin) and the binding; returns the library's path."""
-    _build_binding(force, verbose)
+def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False, checked: bool = True,
+          binding: bool = True) -> str:
+    """Builds the library (and, unless checked=False, its checked twin; unless binding=False, the serving calls'
+    binding); returns the library's path."""
     _build_one(LIB, [], force, ptxas_info, verbose)
     if checked:
         _build_one(LIB_CHECKED, ["-DSAGE_CHECKED"], force, ptxas_info, verbose)
+    if binding:
+        _build_binding(force, verbose)
     return LIB
 
 
 if __name__ == "__main__":
     build(force="--force" in sys.argv, ptxas_info="--ptxas-info" in sys.argv, verbose=True,
-          checked="--no-checked" not in sys.argv)
+          checked="--no-checked" not in sys.argv, binding="--no-binding" not in sys.argv)
