@@ -951,7 +951,7 @@ cudaError_t launch_wait_probe(long long budget_cycles, cudaStream_t st) {
 
 cudaError_t read_clear_device_error(int* value) {
   cudaError_t e = cudaMemcpyFromSymbol(value, g_device_error, sizeof(int));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || *value == 0) return e;  // nothing to clear: one copy less
   const int zero = 0;
   return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
 }

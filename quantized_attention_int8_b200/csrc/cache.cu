@@ -37,7 +37,7 @@ __device__ int g_cache_error = 0;
 
 cudaError_t read_clear_cache_error(int* value) {
   cudaError_t e = cudaMemcpyFromSymbol(value, g_cache_error, sizeof(int));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || *value == 0) return e;  // nothing to clear: one copy less
   const int zero = 0;
   return cudaMemcpyToSymbol(g_cache_error, &zero, sizeof(int));
 }

@@ -45,7 +45,7 @@ __device__ int g_decode_error = 0;
 
 cudaError_t read_clear_decode_error(int* value) {
   cudaError_t e = cudaMemcpyFromSymbol(value, g_decode_error, sizeof(int));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || *value == 0) return e;  // nothing to clear: one copy less
   const int zero = 0;
   return cudaMemcpyToSymbol(g_decode_error, &zero, sizeof(int));
 }

@@ -39,7 +39,7 @@ __device__ int g_quant_error = 0;
 
 cudaError_t read_clear_quant_error(int* value) {
   cudaError_t e = cudaMemcpyFromSymbol(value, g_quant_error, sizeof(int));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || *value == 0) return e;  // nothing to clear: one copy less
   const int zero = 0;
   return cudaMemcpyToSymbol(g_quant_error, &zero, sizeof(int));
 }
