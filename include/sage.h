@@ -289,8 +289,9 @@ typedef struct {
 
 /* Quantizes new tokens into the cache.  k and v: (T, Hkv, d) packed tokens; cu_seqlens: DEVICE int32 [B + 1]
  * non-decreasing offsets from 0 to at most T (sequence b owns tokens cu_seqlens[b] .. cu_seqlens[b+1]-1; tokens at and
- * behind cu_seqlens[B] are left alone; a table that breaks this is reported by sage_check_status as
- * SAGE_ERR_INVALID_ARG and the tokens that meet the fault are skipped), NULL: T = B, one token per sequence.  seq_lens: DEVICE int32 [B], the lengths WITH
+ * behind cu_seqlens[B] are left alone; a token that meets a table that breaks this, a negative or too large
+ * cu_seqlens[B] or a first offset that is not 0 among it, is skipped and reported by sage_check_status as
+ * SAGE_ERR_INVALID_ARG), NULL: T = B, one token per sequence.  seq_lens: DEVICE int32 [B], the lengths WITH
  * the new tokens: token i of sequence b goes to position seq_lens[b] - (new tokens of b) + i.  Without cu_seqlens,
  * a sequence of length 0 is an empty slot of the batch and is skipped.  Per token and kv head, in fp32:
  *   y = k - k_mean (k_mean: DEVICE fp32 [Hkv][d], NULL: 0; the same for all tokens of a head, it adds one

@@ -227,11 +227,14 @@ __device__ __forceinline__ void code_scale(float amax, float top, float* scale, 
 
 // The sequence of packed token t (of `total`), and that sequence's first token and token count.  The first
 // probe finds it in a batch with one token each; otherwise a binary search over the offsets.  false:
-// t is behind the last sequence, or (flagged) the offsets are not non-decreasing from 0 to at most total.
+// t is behind the last sequence, or (flagged) it meets offsets that do not go from 0 to at most total without falling.
 __device__ __forceinline__ bool find_sequence(const int32_t* cu, int B, int t, int total, int* b_out, int* first,
                                               int* count) {
   const int end = cu[B];
-  if (t >= end && end <= total) return false;
+  if (t >= end && end >= 0 && end <= total) {
+    if (cu[0] != 0) atomicOr(&g_cache_error, kBadArg);
+    return false;
+  }
   int b = min(B - 1, t);
   if (!(cu[b] <= t && t < cu[b + 1])) {
     int lo = 0, hi = B - 1;  // the last b with cu[b] <= t
