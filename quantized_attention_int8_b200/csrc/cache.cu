@@ -657,8 +657,10 @@ cudaError_t launch_rows(HeadRowsParams p, cudaStream_t st) {
   const auto heads = [&](const HeadRows& k) { return heads_at_a_time(HC, p.append, (int)(&k - p.kind)); };
   unsigned all = 0;
   double cost = 0;
-  // a round's time: coded keys 1.45 and values 1.1 times queries' per row (bf16, d 128, norm and rotation)
-  const double weight[3] = {1.0, p.append ? 1.45 * heads_at_a_time(HC, true, kK) / HC : 1.0, 1.1};
+  // A round's time: coded keys 1.9 and values 1.1 times queries' per row.  Measured with Hq32 Hkv8 and norm, rotation and k_mean,
+  // keys at 1.45, 1.9 and 2.6: 8 x 256 tokens d 128 15.6, 14.5, 14.2 us; 8 x 128 d 256 15.6, 14.6, 14.2; without k_mean
+  // 8 x 512 d 64 13.9, 13.9, 14.7, 2 x 700 d 128 10.9, 10.4, 10.8.
+  const double weight[3] = {1.0, p.append ? 1.9 * heads_at_a_time(HC, true, kK) / HC : 1.0, 1.1};
   for (HeadRows& k : p.kind) {
     k.chunks = (k.H + heads(k) - 1) / heads(k), all += rounds_of(k);
     cost += rounds_of(k) * weight[&k - p.kind];
