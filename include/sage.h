@@ -340,7 +340,8 @@ sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long 
                              sage_dtype dtype, float sm_scale, void* stream);
 
 /* Synchronizes `stream`, then reports (and clears) the device-side error word:
- * SAGE_ERR_TIMEOUT if a kernel gave up on a bounded wait, SAGE_ERR_BOUNDS if a
+ * SAGE_ERR_TIMEOUT if a kernel gave up on a bounded wait (what its call wrote is
+ * then not to be used), SAGE_ERR_BOUNDS if a
  * kernel of the checked build skipped a store outside its buffer (see
  * sage_checked_build), SAGE_ERR_INVALID_ARG for a flagged tile record,
  * cu_seqlens table, page, position or length, SAGE_ERR_CUDA for a pending CUDA error.  The error word is one per device, not per stream: it collects the

@@ -939,13 +939,18 @@ sage_status sage_attn_decode(const void* q, long long q_batch_stride, long long 
   p.x_out = limited_extent(out, out_bytes);
   if ((s = check_device()) != SAGE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // How the work is cut and shared out (times: Hq32, Hkv8, d128, bf16).  Sequences of up to 512 keys are not split at all: the
-  // join takes as long as the keys that it saves a CTA (B1: 12.8 and 12.9 us at 500 keys, 14.6 and 18.4 us at
-  // 1000), and a second launch and a workspace; every pair has a CTA (B64, 500 keys: 26.9 us, in one wave of CTAs
-  // with two pairs each 29.3).  Longer ones in units of 256 keys, a CTA to each, where those are no more than the
-  // CTAs that run at the same time (B1, 4000 keys: 15.8 us, in units of 64 19.3).  Else that many CTAs share units
-  // of 64 keys evenly.  A pair then counts for as many more units as take the time that a CTA needs to begin
-  // and end with it, 4 to 6 us (B64, 1 to 1000 keys: 51.7 us without, 32.5 with; B64, 1 to 16384: 210 and 191).
+  // How the work is cut and shared out (times: Hq32, Hkv8, d128, bf16, calls in a graph).  Sequences of up to 512 keys are not
+  // split at all: every pair has a CTA, and there is no join and no workspace.  One sequence: 500 keys 8.7 us, split 9.4;
+  // 700 keys 9.4 split, 11.4 not; 16 sequences of 500 8.9 and 12.3, 64 of 500 20.2 and 24.7.  (With many pairs the limit
+  // could be higher: 16 sequences of 1000 keys 17.8 us, not split 14.5; 64 of 1000 36.5 and 37.8.)
+  // Longer ones go in units of 256 keys, a CTA to each, where those are no more than the CTAs that run at the same time (one
+  // of 4000 keys: 10.3 us, in units of 64 10.9, of 512 12.3; four of 2000: 11.6, 13.0, 12.8).  Else that many CTAs
+  // share units of 64 keys evenly (64 of 1 to 1000: 25.9 us, of 32 27.4, of 128 27.0).  A pair then counts for as
+  // many more units as take the time that a CTA needs to begin and end with it (64 of 1 to 1000, without and with: d 64
+  // 44.1 and 21.6 us, d 128 43.6 and 25.9, d 256 62.2 and 41.5; 64 of 1 to 16384: 150 and 138, 212 and 208, 401 and 387; 4 to
+  // 8 units are within 9% of these).
+  // All of it goes by max_seqlen, since the lengths are on the device: 16 sequences of 200 keys take 12.1 us under a bound of
+  // 4096, and 6.0 not split.
   const long long most = 148LL * decode_ctas_per_sm(p.d);
   const auto units = [&] {
     const long long keys = std::max<long long>(1, ((long long)p.max_len + (1 << p.unit_log2) - 1) >> p.unit_log2);

@@ -15,7 +15,9 @@
 // 8192-token prompts (Hq32 Hkv8 d128 fp16 with norm, rotation and k_mean, 740 MB) takes 160 us, 4.6
 // TB/s: the coded rows are a third of the rows and over half of the instructions; HBM is 57% busy and 2.5 of 4
 // instructions issue per cycle, with load and fixed latencies the largest stalls.  The read back of 16 prefixes (1 to 8192 tokens, Hkv8 d128, 401 MB) takes
-// 75 us, 5.3 TB/s: the loads' latency, at 20 warps to an SM.  Short calls are launch latency: 4 to 5 us.
+// 75 us, 5.3 TB/s: the loads' latency, at 20 warps to an SM.  Short calls are launch latency: 4 us in a graph, 5.1 to
+// 5.8 us through the package.  Heads of 40, 80 and 160 channels leave 3 of 8 lanes idle (norm and rotation of heads of 40, 80,
+// 96, 128 and 160 channels, 0.34 GB each: 3.7, 3.7, 4.3, 5.3 and 3.8 TB/s).
 //
 // A row (one head of one token) is
 // owned by 8, 16 or 32 consecutive lanes, eight channels to a lane, so that the sum of squares and

@@ -5,8 +5,11 @@
 //
 // One pass over the cache with a running reference and sum per query head.  The codes are read once
 // and are most of the bytes: 2 d + 8 per key and kv head against 4 d G operations (G query heads share
-// a kv head), so HBM bounds it for every G that a tile holds: B32 L16384 Hq32 Hkv8 d128 bf16 (1107 MB) takes 187 us,
-// 5.9 TB/s (fp16, with a second P term, 196 us); of that about 10 us are the beginning and the end.
+// a kv head), so HBM bounds it for every G that a tile holds where the heads fill their instance (64, 128 or 256 channels):
+// B32 L16384 Hq32 Hkv8 d128 bf16 (1107 MB) takes 182 us, 6.1 TB/s (fp16, with a second P term, 196 us); of that about 10 us
+// are the beginning and the end.  At 64 channels the work per key is the same for half the bytes (4.3 TB/s of 0.57 GB),
+// padded heads do the products of the channels that they do not have (80 and 160: 3.9 and 3.8 TB/s), and
+// codes are widened once per tile (16 heads to a kv head 3.1 TB/s, 32 1.6).
 //
 // Keys are the M rows of both products, query heads the N columns (tiles of 8):
 //   S^T = K Q^T       m16n8k16, A = 16 keys x 16 channels, codes widened exactly to fp16
