@@ -13,7 +13,7 @@
 // Everything here moves bytes: about ten operations per element.  Norm and rotation of the video-DiT heads (B1
 // N32768 Hq24 Hkv24 d128 bf16, 822 MB) take 133 us, 6.2 TB/s: HBM bounds them.  The write of four
 // 8192-token prompts (Hq32 Hkv8 d128 fp16 with norm, rotation and k_mean, 740 MB) takes 160 us, 4.6
-// TB/s: the coded rows are a third of the rows and over half of the instructions; HBM is 57% busy and 2.5 of 4
+// TB/s: the coded rows are a third of the rows and over half of the instructions; HBM is 55% busy and 2.6 of 4
 // instructions issue per cycle, with load and fixed latencies the largest stalls.  The read back of 16 prefixes (1 to 8192 tokens, Hkv8 d128, 401 MB) takes
 // 75 us, 5.3 TB/s: the loads' latency, at 20 warps to an SM.  Short calls are launch latency: 4 us in a graph, 5.1 to
 // 5.8 us through the package.  Heads of 40, 80 and 160 channels leave 3 of 8 lanes idle (norm and rotation of heads of 40, 80,
