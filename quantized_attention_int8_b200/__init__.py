@@ -331,7 +331,8 @@ def sage_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weigh
     holds the rot/2 cosines of position p's angles, then the sines; channels i and i + rot/2 turn together, or
     2i and 2i + 1 with interleaved; None: no rotation.  positions int32 (N,) or (B,N), default 0..N-1; one
     outside the table leaves its token unwritten and is reported by sage_check_status.  Weights (d,) in fp16,
-    bf16 or fp32.  q_out may be q and k_out may be k."""
+    bf16 or fp32.  q_out may be q and k_out may be k; outputs that overlap q, k or each other otherwise are refused
+    (slices side by side of one fused tensor do not)."""
     if tensor_layout not in _LAYOUTS:
         raise ValueError(f"tensor_layout must be 'HND' or 'NHD', got {tensor_layout!r}")
     r = _serving().qk_norm_rope(capi.serving["sage_qk_norm_rope"], q, k, positions, tensor_layout == "HND", cos_sin,
@@ -361,7 +362,7 @@ def sage_cache_append(cache, k, v, page_table, seq_lens, cu_seqlens=None, q=None
     norm, weights, cos_sin, interleaved: as sage_qk_norm_rope, on the keys at their positions, and on q (T,Hq,d),
     which is returned (q_out; None without q).  k_mean float32 (Hkv,d) is subtracted from the keys before
     they are coded.  Channels contiguous, other strides free.  Bad pages and positions are skipped and reported
-    by sage_check_status."""
+    by sage_check_status.  q_out may be q; it must not overlap k, v or the cache (refused)."""
     r = _serving().cache_append(capi.serving["sage_cache_append"], cache["k8"], cache["ks"], cache["v8"], cache["vs"], k, v,
                                 page_table, seq_lens, cu_seqlens, q, cos_sin, q_weight, k_weight, norm, eps, interleaved,
                                 k_mean, q_out)
